@@ -67,7 +67,12 @@ typedef enum {
     SPEC_ERR_UNSUPPORTED = 4  /* a size beyond the supported maximum */
 } spec_status_t;
 
-typedef enum { SPEC_DTYPE_F32 = 0, SPEC_DTYPE_BF16 = 1, SPEC_DTYPE_F16 = 2 } spec_dtype_t;
+typedef enum {
+    SPEC_DTYPE_F32 = 0,
+    SPEC_DTYPE_BF16 = 1,
+    SPEC_DTYPE_F16 = 2,
+    SPEC_DTYPE_E4M3 = 3 /* 8-bit float (4 exponent, 3 mantissa bits), in KV caches only */
+} spec_dtype_t;
 
 /* Bits of err_flags[b]. */
 #define SPEC_ERRF_BAD_TOKEN 1 /* a draft / node token outside [0, V) */
@@ -75,6 +80,9 @@ typedef enum { SPEC_DTYPE_F32 = 0, SPEC_DTYPE_BF16 = 1, SPEC_DTYPE_F16 = 2 } spe
 #define SPEC_ERRF_TIMEOUT 4   /* a bounded device wait gave up (should never happen) */
 #define SPEC_ERRF_BAD_TREE 8  /* parents[0] != -1 or parents[i] not in [0, i) */
 #define SPEC_ERRF_BAD_TEMPERATURE 16 /* a per-request temperature that is NaN, negative or infinite */
+#define SPEC_ERRF_BAD_LENGTH 32  /* a history, prompt, context or chunk length out of range */
+#define SPEC_ERRF_BAD_SLOT 64    /* a cache slot or page outside the cache */
+#define SPEC_ERRF_BAD_PENALTY 128 /* a penalty that is NaN or infinite, or a repetition penalty <= 0 */
 
 /* Largest supported sizes. */
 #define SPEC_MAX_K 256           /* draft tokens per request (chain / n-gram) */
@@ -83,6 +91,9 @@ typedef enum { SPEC_DTYPE_F32 = 0, SPEC_DTYPE_BF16 = 1, SPEC_DTYPE_F16 = 2 } spe
 #define SPEC_MAX_WALK_VOCAB 262144 /* V for spec_verify_tree_walk */
 #define SPEC_MAX_NGRAM 32          /* n_max for spec_ngram_draft */
 #define SPEC_MAX_KV_CACHES 1024    /* caches (layers x K/V) per spec_kv_compact call */
+#define SPEC_MAX_LOGITS_ROWS 1024  /* rows per request for spec_logits_process */
+#define SPEC_MAX_BIASES 4096       /* bias entries per request for spec_logits_process */
+#define SPEC_MAX_KV_HEAD_DIM 256   /* head_dim for spec_kv_write / spec_kv_read */
 
 /* Bytes of workspace for a call on B requests with vocabulary V of `dtype`, where
  * rows_per_request is the number of logits rows the call reads per request:
@@ -296,6 +307,145 @@ spec_status_t spec_kv_compact(void *const *caches, int num_caches, long long num
                               const int32_t *parents, const int32_t *accept_len,
                               const int32_t *path_nodes, int32_t *err_flags,
                               spec_stream_t stream);
+
+/*
+ * Logits processing ahead of verification: penalties for repeated tokens, biases and grammar masks
+ * on the target's logits of a draft chain or tree (the x078.com page's production section sets
+ * sampling parameters per request).  Row n of request b scores the token after draft position (or
+ * node) n, so the tokens its penalties count are the request's history AND the draft tokens on
+ * n's own path.  Verifying the processed rows is lossless with respect to decoding one token at a
+ * time under the same rules.
+ *
+ * With c = the occurrences of token i in the output part of the history plus those on the path,
+ * and x the logit:
+ *   if i occurs in the history or on the path:  x = x > 0 ? x / repetition : x * repetition
+ *   if c > 0:                                   x = x - (frequency * c + presence)
+ *   x = x + the sum, in list order, of i's biases
+ *   if the row's mask does not allow i:         x = -inf (whatever x was, NaN included)
+ * in 32 bits, each step rounded to nearest, and rounded once more to dtype at the end.  Tokens
+ * that no rule touches keep their bits.  A row whose mask allows nothing becomes all -inf, which
+ * the verification calls report as SPEC_ERRF_NONFINITE.
+ *
+ * logits         [B][R][V] dtype; R = K + 1 rows of a chain or N + 1 of a tree.
+ * history        [B][Lmax] int32 or NULL (Lmax 0): prompt and output so far, the last accepted
+ *                token (a tree's root) included; ids outside [0, V) are ignored.
+ * history_len    [B] int32 in [0, Lmax] (required with history).
+ * prompt_len     [B] int32 in [0, history_len] or NULL (0): how much of the history is prompt.
+ *                Another length fails the request with SPEC_ERRF_BAD_LENGTH.
+ * draft_tokens   [B][R-1] int32 or NULL: a chain; row k's path is the first k draft tokens.
+ * node_tokens    [B][R] (entry 0 ignored) and parents [B][R] int32, or NULL: a tree, as for
+ *                spec_verify_tree_greedy; row n's path is n and its ancestors but the root.
+ *                Give a chain, a tree or neither (no path), not both.
+ * repetition, presence, frequency  [B] float or NULL (1, 0, 0).
+ * bias_tokens    [B][num_biases] int32 (ids outside [0, V): unused entries) and bias_values
+ *                [B][num_biases] float; NULL when num_biases is 0.
+ * allowed        [B][R][ceil(V / 32)] uint32 or NULL: bit i % 32 of word i / 32 allows token i.
+ * out            [B][R][V] dtype: may be logits itself (in place: only the vectors that a rule
+ *                touches are read and written), otherwise must not overlap it.
+ * err_flags      [B] int32 or NULL: SPEC_ERRF_BAD_LENGTH, SPEC_ERRF_BAD_TREE, SPEC_ERRF_BAD_TOKEN
+ *                (a draft or node token outside [0, V)), SPEC_ERRF_BAD_PENALTY; the rows of such a
+ *                request come out unprocessed.
+ * Limits: R <= SPEC_MAX_LOGITS_ROWS, num_biases <= SPEC_MAX_BIASES, B <= 65535.  One kernel launch; no workspace.
+ */
+spec_status_t spec_logits_process(const void *logits, spec_dtype_t dtype, int B, int R, int V,
+                                  const int32_t *history, const int32_t *history_len,
+                                  const int32_t *prompt_len, int Lmax,
+                                  const int32_t *draft_tokens, const int32_t *node_tokens,
+                                  const int32_t *parents, const float *repetition,
+                                  const float *presence, const float *frequency,
+                                  const int32_t *bias_tokens, const float *bias_values,
+                                  int num_biases, const uint32_t *allowed, void *out,
+                                  int32_t *err_flags, spec_stream_t stream);
+
+/*
+ * Writing new K and V rows into their cache slots, quantised when the cache is e4m3 (the commit of
+ * tokens to the KV cache of the vikram-blog.pages.dev page's diagram, before compaction).
+ *
+ * e4m3 caches hold, per slot and KV head, D codes and one scale s, the smallest power of two (at
+ * least 2^-126) with max |x| <= 448 s; the codes are x / s rounded to nearest even.  A power of two
+ * makes the scaling, and reading back in 32 or bf16 bits, exact: the code is the only rounding.
+ * The maximum is taken over finite elements; NaN and infinities are stored as NaN.
+ * Caches of the inputs' own dtype take the rows' bits.
+ *
+ * k, v           token n = b T + t at k + n k_stride (elements): num_kv_heads rows of head_dim
+ *                contiguous elements; strides >= num_kv_heads * head_dim, 16-byte multiples, and
+ *                16-byte aligned pointers (slices of a fused projection, say).
+ * slots          [B][T] int32: each token's slot; -1 for no token (nothing is written).  Distinct:
+ *                which of two tokens with one slot ends up there is undefined, row by row.
+ * k_cache, v_cache  [num_slots][num_kv_heads][head_dim] cache_dtype (dtype, or SPEC_DTYPE_E4M3).
+ * k_scale, v_scale  [num_slots][num_kv_heads] float, e4m3 only (else ignored).
+ * err_flags      [B] int32 or NULL: SPEC_ERRF_BAD_SLOT when a slot is outside [-1, num_slots); that
+ *                token is skipped, the others are written.
+ * Limits: head_dim a multiple of 8, at most SPEC_MAX_KV_HEAD_DIM.  One kernel launch; no workspace.
+ * The caches and scales are plain arrays of rows, which spec_kv_compact can move: rows of
+ * num_kv_heads * head_dim elements, and of 4 num_kv_heads bytes (a multiple of 16 for compaction).
+ */
+spec_status_t spec_kv_write(const void *k, const void *v, spec_dtype_t dtype, long long k_stride,
+                            long long v_stride, int B, int T, int num_kv_heads, int head_dim,
+                            const int32_t *slots, void *k_cache, void *v_cache,
+                            spec_dtype_t cache_dtype, float *k_scale, float *v_scale,
+                            long long num_slots, int32_t *err_flags, spec_stream_t stream);
+
+/*
+ * Reading cache rows back: the values code * s of an e4m3 cache rounded once to dtype, or the
+ * bits of a cache of that dtype.  A token with slot -1, or a bad one (SPEC_ERRF_BAD_SLOT), reads
+ * zeros.  k_out, v_out: [B][T][num_kv_heads][head_dim] dtype, 16-byte aligned.  Otherwise as
+ * spec_kv_write; slots need not be distinct.
+ */
+spec_status_t spec_kv_read(const void *k_cache, const void *v_cache, spec_dtype_t cache_dtype,
+                           const float *k_scale, const float *v_scale, long long num_slots, int B,
+                           int T, int num_kv_heads, int head_dim, const int32_t *slots,
+                           void *k_out, void *v_out, spec_dtype_t dtype, int32_t *err_flags,
+                           spec_stream_t stream);
+
+/*
+ * The target's attention of a chunk of new tokens (a draft chain, a flattened draft tree, one token
+ * or a piece of a prompt) over a paged KV cache: section III.2 of the page named at the top, the
+ * tree's attention mask.  Grouped queries: head h reads KV head h / (num_heads / num_kv_heads).
+ *
+ * Position j of request b lies in page page_table[b][j / page_size], at row j % page_size.  The
+ * committed prefix is positions 0 .. context_len[b] - 1; chunk token t lies at position
+ * context_len[b] + t (its K and V written before, by spec_kv_write say).  Token t attends to the
+ * whole prefix and, in the chunk, to tokens 0..t (parents NULL) or to itself and its ancestors.
+ *   out[b][t][h] = sum_j softmax_j(scale q . k_j) v_j
+ * with the scores, the softmax statistics and the sums in 32 bits; the weights are rounded to
+ * dtype before they multiply V, and the result is rounded once.
+ *
+ * q              token n = b T + t at q + n q_stride (elements; a 16-byte multiple, pointer
+ *                16-byte aligned): num_heads rows of head_dim elements, bf16 or f16 (f32:
+ *                SPEC_ERR_UNSUPPORTED).
+ * k_cache, v_cache  [num_pages][page_size][num_kv_heads][head_dim] of dtype or e4m3 (the layout of
+ *                spec_kv_write: slot = page * page_size + row), 16-byte aligned; e4m3 with k_scale,
+ *                v_scale [num_pages][page_size][num_kv_heads].
+ * page_table     [B][pages_per_request] int32; entries behind the last position are not read.
+ * context_len    [B] int32 >= 0.
+ * chunk_len      [B] int32 in [0, T] or NULL (T): the request's tokens; rows of out and lse behind
+ *                them are left as they were.  context_len + chunk_len must fit the page table:
+ *                otherwise SPEC_ERRF_BAD_LENGTH.
+ * parents        [B][T] int32 or NULL, as for spec_verify_tree_greedy (checked over the request's
+ *                chunk_len tokens): SPEC_ERRF_BAD_TREE.
+ * scale          > 0 and finite.
+ * out            [B][T][num_heads][head_dim] dtype, 16-byte aligned.
+ * lse            [B][T][num_heads] float or NULL: log sum_j exp(scale q . k_j).
+ * err_flags      [B] int32 or NULL.  A request with a bad length or tree gets zeros (lse -inf).  A
+ *                page outside [0, num_pages) sets SPEC_ERRF_BAD_SLOT; its rows are read as zeros.
+ * Masked and unwritten places never matter: a NaN or infinity in the K or V row of a token makes
+ * the outputs of the queries that attend to it non-finite, in some or all dimensions, and of no
+ * other query.
+ * workspace      spec_attention_workspace_bytes(...), 256-byte aligned; needs no initialisation and
+ *                holds nothing between calls, but calls that may run concurrently need one each.
+ * Limits: head_dim 64 or 128; page_size a power of two >= 8; T <= SPEC_MAX_WALK_NODES with parents.
+ */
+size_t spec_attention_workspace_bytes(int T, int num_heads, int num_kv_heads, int head_dim);
+spec_status_t spec_attention(const void *q, spec_dtype_t dtype, long long q_stride, int B, int T,
+                             int num_heads, int num_kv_heads, int head_dim, const void *k_cache,
+                             const void *v_cache, spec_dtype_t cache_dtype, const float *k_scale,
+                             const float *v_scale, long long num_pages, int page_size,
+                             const int32_t *page_table, int pages_per_request,
+                             const int32_t *context_len, const int32_t *chunk_len,
+                             const int32_t *parents, float scale, void *out, float *lse,
+                             int32_t *err_flags, void *workspace, size_t workspace_bytes,
+                             spec_stream_t stream);
 
 /*
  * spec_verify_chain without a workspace argument, for callers that cannot allocate device memory

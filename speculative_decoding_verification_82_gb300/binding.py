@@ -18,13 +18,17 @@ from .build import LIB_PATH
 
 SPEC_OK, SPEC_ERR_INVALID_ARG, SPEC_ERR_CUDA, SPEC_ERR_WORKSPACE, SPEC_ERR_UNSUPPORTED = range(5)
 ERRF_BAD_TOKEN, ERRF_NONFINITE, ERRF_TIMEOUT, ERRF_BAD_TREE, ERRF_BAD_TEMPERATURE = 1, 2, 4, 8, 16
+ERRF_BAD_LENGTH, ERRF_BAD_SLOT, ERRF_BAD_PENALTY = 32, 64, 128
 MAX_K, MAX_TREE_NODES, MAX_WALK_NODES, MAX_WALK_VOCAB, MAX_NGRAM = 256, 4096, 1024, 262144, 32
-MAX_KV_CACHES = 1024
+MAX_KV_CACHES, MAX_LOGITS_ROWS, MAX_BIASES, MAX_KV_HEAD_DIM = 1024, 1024, 4096, 256
 DTYPE_CODE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+E4M3 = torch.float8_e4m3fn
+CACHE_CODE = {**DTYPE_CODE, E4M3: 3}
 
 EXPORTED = ("spec_verify_workspace_bytes", "spec_verify_workspace_reset", "spec_verify_chain",
             "spec_verify_ngram", "spec_verify_tree_greedy", "spec_verify_tree_walk", "spec_ngram_draft",
-            "spec_kv_compact",
+            "spec_kv_compact", "spec_kv_write", "spec_kv_read", "spec_logits_process",
+            "spec_attention", "spec_attention_workspace_bytes",
             "spec_verify_chain_static", "spec_status_string")
 STATIC_WORKSPACE_BYTES = 4 << 20
 
@@ -61,6 +65,17 @@ def library(path: str | None = None) -> ctypes.CDLL:
     lib.spec_ngram_draft.restype = I
     lib.spec_kv_compact.argtypes = [ctypes.POINTER(c_void_p), I, ctypes.c_longlong, I, I, I, P, P, P, P, P, P]
     lib.spec_kv_compact.restype = I
+    LL = ctypes.c_longlong
+    lib.spec_kv_write.argtypes = [P, P, I, LL, LL, I, I, I, I, P, P, P, I, P, P, LL, P, P]
+    lib.spec_kv_write.restype = I
+    lib.spec_kv_read.argtypes = [P, P, I, P, P, LL, I, I, I, I, P, P, P, I, P, P]
+    lib.spec_kv_read.restype = I
+    lib.spec_logits_process.argtypes = [P, I, I, I, I, P, P, P, I, P, P, P, P, P, P, P, P, I, P, P, P, P]
+    lib.spec_logits_process.restype = I
+    lib.spec_attention_workspace_bytes.argtypes = [I, I, I, I]
+    lib.spec_attention_workspace_bytes.restype = Z
+    lib.spec_attention.argtypes = [P, I, LL, I, I, I, I, I, P, P, I, P, P, LL, I, P, I, P, P, P, F, P, P, P, P, Z, P]
+    lib.spec_attention.restype = I
     lib.spec_verify_chain_static.argtypes = [P, P, I, I, I, I, F, P, P, P, P, P, P, P, P]
     lib.spec_verify_chain_static.restype = I
     lib.spec_status_string.argtypes = [I]
@@ -308,3 +323,199 @@ def spec_kv_compact(caches, slots, parents, accept_len, path_nodes, *, err_flags
                              _ptr(path_nodes), _ptr(ef), _stream(dev))
     _check(st)
     return ef
+
+
+def _call(fn, device, *args) -> None:
+    """fn(*args, the current stream of `device`) with `device` current, its status checked."""
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(device)))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, _stream(device)))
+
+
+def _cuda(t, name: str):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device, got {t.device}")
+    return t.device
+
+
+def spec_logits_process(logits, *, history=None, history_len=None, prompt_len=None, draft_tokens=None,
+                        node_tokens=None, parents=None, repetition=None, presence=None, frequency=None,
+                        bias_tokens=None, bias_values=None, allowed=None, out=None) -> dict:
+    """Penalties, biases and grammar masks on the logits rows [B][R][V] of a draft chain
+    (`draft_tokens` [B][R-1]) or tree (`node_tokens`, `parents` [B][R]).  out["logits"] may be
+    `logits` itself (in place).  See spec_verify.h."""
+    lib = library()
+    dev = _cuda(logits, "logits")
+    if logits.dtype not in DTYPE_CODE or logits.dim() != 3:
+        raise TypeError("logits must be a [B][R][V] float32/bfloat16/float16 tensor")
+    B, R, V = logits.shape
+    _need(logits, "logits", None, (B, R, V), dev)
+    i32, f32 = torch.int32, torch.float32
+    Lmax = 0
+    if history is not None:
+        if not isinstance(history, torch.Tensor) or history.dim() != 2:
+            raise ValueError("history must be a [B][Lmax] tensor")
+        Lmax = history.shape[1]
+        _need(history, "history", i32, (B, Lmax), dev)
+        _need(history_len, "history_len", i32, (B,), dev)
+    elif history_len is not None or prompt_len is not None:
+        raise ValueError("history_len and prompt_len need a history")
+    _opt(prompt_len, "prompt_len", i32, (B,), dev)
+    if draft_tokens is not None and node_tokens is not None:
+        raise ValueError("give draft_tokens (a chain) or node_tokens and parents (a tree), not both")
+    if (node_tokens is None) != (parents is None):
+        raise ValueError("node_tokens and parents go together")
+    _opt(draft_tokens, "draft_tokens", i32, (B, R - 1), dev)
+    _opt(node_tokens, "node_tokens", i32, (B, R), dev)
+    _opt(parents, "parents", i32, (B, R), dev)
+    _opt(repetition, "repetition", f32, (B,), dev)
+    _opt(presence, "presence", f32, (B,), dev)
+    _opt(frequency, "frequency", f32, (B,), dev)
+    nb = 0
+    if (bias_tokens is None) != (bias_values is None):
+        raise ValueError("bias_tokens and bias_values go together")
+    if bias_tokens is not None:
+        if not isinstance(bias_tokens, torch.Tensor) or bias_tokens.dim() != 2:
+            raise ValueError("bias_tokens must be a [B][num_biases] tensor")
+        nb = bias_tokens.shape[1]
+        _need(bias_tokens, "bias_tokens", i32, (B, nb), dev)
+        _need(bias_values, "bias_values", f32, (B, nb), dev)
+    _opt(allowed, "allowed", i32, (B, R, (V + 31) // 32), dev)
+    out = out or {}
+    o = _out(out.get("logits"), "out logits", logits.dtype, (B, R, V), dev)
+    ef = _out(out.get("err_flags"), "err_flags", i32, (B,), dev)
+    a, z, n = logits.data_ptr(), o.data_ptr(), logits.numel() * logits.element_size()
+    if a != z and a < z + n and z < a + n:
+        raise ValueError("out logits must be logits itself or not overlap it")
+    _call(lib.spec_logits_process, dev, _ptr(logits), DTYPE_CODE[logits.dtype], B, R, V, _ptr(history),
+          _ptr(history_len), _ptr(prompt_len), Lmax, _ptr(draft_tokens), _ptr(node_tokens), _ptr(parents),
+          _ptr(repetition), _ptr(presence), _ptr(frequency), _ptr(bias_tokens), _ptr(bias_values), nb,
+          _ptr(allowed), _ptr(o), _ptr(ef))
+    return dict(logits=o, err_flags=ef)
+
+
+def _kv_caches(k_cache, v_cache, k_scale, v_scale, dtype, dev):
+    """Checks a pair of caches [..., H, D] (slots, or pages and rows, in front); returns slots, H, D."""
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() not in (3, 4):
+        raise ValueError("k_cache must be [num_slots][H][D] or [num_pages][page_size][H][D]")
+    if k_cache.dtype not in (dtype, E4M3):
+        raise TypeError(f"the caches must be {dtype} or {E4M3}, got {k_cache.dtype}")
+    _need(k_cache, "k_cache", None, k_cache.shape, dev)
+    _need(v_cache, "v_cache", k_cache.dtype, k_cache.shape, dev)
+    if k_cache.dtype == E4M3:
+        _need(k_scale, "k_scale", torch.float32, k_cache.shape[:-1], dev)
+        _need(v_scale, "v_scale", torch.float32, k_cache.shape[:-1], dev)
+    elif k_scale is not None or v_scale is not None:
+        raise ValueError("scales belong to e4m3 caches")
+    H, D = k_cache.shape[-2:]
+    slots = k_cache.shape[0] * (k_cache.shape[1] if k_cache.dim() == 4 else 1)
+    return slots, H, D
+
+
+def _token_stride(t, name: str, B: int, T: int, H: int, D: int, dev) -> int:
+    """Elements between consecutive tokens of a [B][T][H][D] tensor whose rows H D are contiguous
+    (a slice of a fused projection, say)."""
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if t.numel() == 0:
+        return H * D
+    s = t.stride()
+    stride = s[1] if T > 1 else s[0] if B > 1 else H * D
+    if (D > 1 and s[3] != 1) or (H > 1 and s[2] != D) or (B > 1 and s[0] != T * stride) or stride < H * D:
+        raise ValueError(f"{name} must hold its tokens at one stride and each token's heads contiguously")
+    return stride
+
+
+def spec_kv_write(k, v, k_cache, v_cache, slots, *, k_scale=None, v_scale=None, err_flags=None) -> torch.Tensor:
+    """Writes K and V rows [B][T][H][D] into the cache slots `slots` [B][T], quantised when the caches
+    are float8_e4m3fn (then with scales).  Returns err_flags [B].  See spec_verify.h."""
+    lib = library()
+    dev = _cuda(k, "k")
+    if k.dtype not in DTYPE_CODE or k.dim() != 4:
+        raise TypeError("k must be a [B][T][H][D] float32/bfloat16/float16 tensor")
+    B, T, H, D = k.shape
+    if not isinstance(v, torch.Tensor) or v.dtype != k.dtype or v.shape != k.shape:
+        raise ValueError("v must have k's shape and dtype")
+    ks, vs = _token_stride(k, "k", B, T, H, D, dev), _token_stride(v, "v", B, T, H, D, dev)
+    S, Hc, Dc = _kv_caches(k_cache, v_cache, k_scale, v_scale, k.dtype, dev)
+    if (Hc, Dc) != (H, D):
+        raise ValueError(f"the caches hold {Hc} heads of {Dc}, k and v {H} of {D}")
+    _need(slots, "slots", torch.int32, (B, T), dev)
+    ef = _out(err_flags, "err_flags", torch.int32, (B,), dev)
+    _call(lib.spec_kv_write, dev, _ptr(k), _ptr(v), DTYPE_CODE[k.dtype], ks, vs, B, T, H, D, _ptr(slots),
+          _ptr(k_cache), _ptr(v_cache), CACHE_CODE[k_cache.dtype], _ptr(k_scale), _ptr(v_scale), S, _ptr(ef))
+    return ef
+
+
+def spec_kv_read(k_cache, v_cache, slots, dtype, *, k_scale=None, v_scale=None, out=None) -> dict:
+    """The rows of the cache slots `slots` [B][T] as `dtype` [B][T][H][D].  See spec_verify.h."""
+    lib = library()
+    dev = _cuda(k_cache, "k_cache")
+    if dtype not in DTYPE_CODE:
+        raise TypeError("dtype must be float32, bfloat16 or float16")
+    S, H, D = _kv_caches(k_cache, v_cache, k_scale, v_scale, dtype, dev)
+    if not isinstance(slots, torch.Tensor) or slots.dim() != 2:
+        raise ValueError("slots must be a [B][T] tensor")
+    B, T = slots.shape
+    _need(slots, "slots", torch.int32, (B, T), dev)
+    out = out or {}
+    ko = _out(out.get("k"), "out k", dtype, (B, T, H, D), dev)
+    vo = _out(out.get("v"), "out v", dtype, (B, T, H, D), dev)
+    ef = _out(out.get("err_flags"), "err_flags", torch.int32, (B,), dev)
+    _call(lib.spec_kv_read, dev, _ptr(k_cache), _ptr(v_cache), CACHE_CODE[k_cache.dtype], _ptr(k_scale), _ptr(v_scale),
+          S, B, T, H, D, _ptr(slots), _ptr(ko), _ptr(vo), DTYPE_CODE[dtype], _ptr(ef))
+    return dict(k=ko, v=vo, err_flags=ef)
+
+
+def attention_workspace_bytes(T: int, num_heads: int, num_kv_heads: int, head_dim: int) -> int:
+    """Workspace bytes of a spec_attention call with chunks of T tokens (any number of requests)."""
+    return int(library().spec_attention_workspace_bytes(T, num_heads, num_kv_heads, head_dim))
+
+
+def make_attention_workspace(T: int, num_heads: int, num_kv_heads: int, head_dim: int, device) -> torch.Tensor:
+    """A workspace for such calls; concurrent calls need one each."""
+    n = max(256, attention_workspace_bytes(T, num_heads, num_kv_heads, head_dim))
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def spec_attention(q, k_cache, v_cache, page_table, context_len, *, chunk_len=None, parents=None, scale=None,
+                   k_scale=None, v_scale=None, workspace=None, out=None, lse=None) -> dict:
+    """Attention of the chunk q [B][T][Hq][D] over the paged caches [num_pages][page_size][H][D]:
+    the prefix of context_len[b] tokens, then the chunk (causal, or by the tree `parents` [B][T]).
+    `scale` is 1 / sqrt(D) unless given; `lse` [B][T][Hq] float32 receives the log-sum-exp.  See
+    spec_verify.h."""
+    lib = library()
+    dev = _cuda(q, "q")
+    if q.dtype not in (torch.bfloat16, torch.float16) or q.dim() != 4:
+        raise TypeError("q must be a [B][T][Hq][D] bfloat16/float16 tensor")
+    B, T, Hq, D = q.shape
+    qs = _token_stride(q, "q", B, T, Hq, D, dev)
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise ValueError("k_cache must be [num_pages][page_size][H][D]")
+    _, H, Dc = _kv_caches(k_cache, v_cache, k_scale, v_scale, q.dtype, dev)
+    if Dc != D or H < 1 or Hq % H != 0:
+        raise ValueError(f"{Hq} query heads of {D} do not fit {H} KV heads of {Dc}")
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must be a [B][pages_per_request] tensor")
+    P = page_table.shape[1]
+    _need(page_table, "page_table", torch.int32, (B, P), dev)
+    _need(context_len, "context_len", torch.int32, (B,), dev)
+    _opt(chunk_len, "chunk_len", torch.int32, (B,), dev)
+    _opt(parents, "parents", torch.int32, (B, T), dev)
+    _opt(lse, "lse", torch.float32, (B, T, Hq), dev)
+    if workspace is None:
+        workspace = make_attention_workspace(T, Hq, H, D, dev)
+    elif not isinstance(workspace, torch.Tensor) or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    out = out or {}
+    o = _out(out.get("out"), "out", q.dtype, (B, T, Hq, D), dev)
+    ef = _out(out.get("err_flags"), "err_flags", torch.int32, (B,), dev)
+    _call(lib.spec_attention, dev, _ptr(q), DTYPE_CODE[q.dtype], qs, B, T, Hq, H, D, _ptr(k_cache), _ptr(v_cache),
+          CACHE_CODE[k_cache.dtype], _ptr(k_scale), _ptr(v_scale), k_cache.shape[0], k_cache.shape[1], _ptr(page_table),
+          P, _ptr(context_len), _ptr(chunk_len), _ptr(parents), D**-0.5 if scale is None else float(scale), _ptr(o),
+          _ptr(lse), _ptr(ef), _ptr(workspace), workspace.numel() * workspace.element_size())
+    return dict(out=o, lse=lse, err_flags=ef)
