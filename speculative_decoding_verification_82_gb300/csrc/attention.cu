@@ -1,144 +1,96 @@
-// attention.cu -- spec_attention: attention of a chunk of new tokens over a paged KV cache (sm_103a).
+// attention.cu -- spec_attention's C entry: argument checks, tensor maps, workspace layout, launch.
 //
-// One warp per (token, head): the online softmax over the prefix, then over the token's own path in
-// the chunk, one position at a time.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_runtime.h>
+// Host side only; the kernels live in attention_kernel.cuh (instantiated per element type in
+// attention_{bf16,f16}.cu).  No call allocates memory or synchronises the host.
+#include <cuda.h>
 #include <limits.h>
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
+
+#include "attention_kernel.cuh"
 #include "spec_verify.h"
+
+namespace specv {
+namespace attn {
+extern template cudaError_t launch_attention<__nv_bfloat16>(const Params&, int, bool, bool, int, cudaStream_t);
+extern template cudaError_t launch_attention<__half>(const Params&, int, bool, bool, int, cudaStream_t);
+}  // namespace attn
+}  // namespace specv
 
 namespace {
 
-constexpr int kWarps = 8;
+using specv::attn::kMaxCtas;
+using specv::attn::kTile;
+using specv::attn::Params;
+using specv::attn::Record;
 
-struct AttnParams {
-  const unsigned char *q, *kc, *vc;
-  const float *ks, *vs;
-  long long q_stride, num_pages;
-  int B, T, Hq, H, page_size, P;
-  const int32_t *table, *context_len, *chunk_len, *parents;
-  float scale;
-  unsigned char* out;
-  float* lse;
-  int32_t* err_flags;
+// Rows of a unit of work: one row tile while a request's rows fit it, else two.
+int unit_rows(long long rows) { return rows > kTile ? 2 * kTile : kTile; }
+
+// Workspace: the partial results' O, their m and l, and the records, in 256-byte aligned regions.
+struct Layout {
+  size_t o, ml, rec, total;
 };
-
-template <typename T>
-__device__ float to_f(T v);
-template <>
-__device__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <>
-__device__ float to_f(__half v) { return __half2float(v); }
-template <typename T>
-__device__ T from_f(float v);
-template <>
-__device__ __nv_bfloat16 from_f(float v) { return __float2bfloat16_rn(v); }
-template <>
-__device__ __half from_f(float v) { return __float2half_rn(v); }
-__device__ __forceinline__ float e4m3(uint8_t c) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
-  return __low2float(*reinterpret_cast<const __half2*>(&h));
+Layout layout(long long rows, int D) {
+  const size_t UR = (size_t)unit_rows(rows), parts = 2 * (size_t)kMaxCtas;
+  Layout L;
+  L.o = 0;
+  L.ml = L.o + parts * UR * (size_t)D * 4;
+  L.rec = L.ml + parts * UR * 8;
+  L.total = (L.rec + kMaxCtas * sizeof(Record) + 255) / 256 * 256;
+  return L;
 }
 
-template <typename T, int D, bool E4M3>
-__global__ void __launch_bounds__(kWarps * 32) attention_kernel(const AttnParams A) {
-  constexpr int N = D / 32;
-  const int b = blockIdx.y, lane = threadIdx.x & 31;
-  const long long L = __ldg(A.context_len + b);
-  const int n = A.chunk_len ? __ldg(A.chunk_len + b) : A.T;
-  int flags = 0;
-  if (L < 0 || n < 0 || n > A.T || L + n > (long long)A.P * A.page_size) flags |= SPEC_ERRF_BAD_LENGTH;
-  const int32_t* par = A.parents ? A.parents + (size_t)b * A.T : nullptr;
-  bool bad = false;
-  if (par && !flags)
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
-      const int p = __ldg(par + i);
-      bad = bad || (i == 0 ? p != -1 : (p < 0 || p >= i));
-    }
-  if (__syncthreads_or(bad)) flags |= SPEC_ERRF_BAD_TREE;
-  const bool failed = flags != 0;
-  if (blockIdx.x == 0 && A.err_flags) {
-    bool slot = false;
-    if (!failed)
-      for (long long j = threadIdx.x; j < (L + n + A.page_size - 1) / A.page_size; j += blockDim.x) {
-        const int p = __ldg(A.table + (size_t)b * A.P + j);
-        slot = slot || p < 0 || p >= A.num_pages;
-      }
-    if (__syncthreads_or(slot)) flags |= SPEC_ERRF_BAD_SLOT;
-    if (threadIdx.x == 0) A.err_flags[b] = flags;
-  }
-  const int G = A.Hq / A.H;
-  for (long long i = (long long)blockIdx.x * kWarps + threadIdx.x / 32; i < (long long)A.T * A.Hq; i += (long long)gridDim.x * kWarps) {
-    const int t = (int)(i / A.Hq), h = (int)(i % A.Hq);
-    if (!failed && t >= n) continue;
-    const int kh = h / G;
-    const size_t o = (((size_t)b * A.T + t) * A.Hq + h) * D;
-    float q[N], acc[N], m = -INFINITY, l = 0.f;
-    const T* qp = reinterpret_cast<const T*>(A.q) + ((long long)b * A.T + t) * A.q_stride + (size_t)h * D;
-    for (int d = 0; d < N; ++d) {
-      q[d] = failed ? 0.f : to_f(qp[d * 32 + lane]) * A.scale;
-      acc[d] = 0.f;
-    }
-    auto attend = [&](long long j) {
-      const int page = __ldg(A.table + (size_t)b * A.P + j / A.page_size);
-      const bool ok = page >= 0 && page < A.num_pages;
-      const size_t r = ok ? ((size_t)page * A.page_size + j % A.page_size) * A.H + kh : 0;
-      float k[N], v[N], s = 0.f;
-      for (int d = 0; d < N; ++d) {
-        const size_t at = r * D + d * 32 + lane;
-        if (!ok) {
-          k[d] = v[d] = 0.f;
-        } else if constexpr (E4M3) {
-          k[d] = e4m3(A.kc[at]) * A.ks[r];
-          v[d] = e4m3(A.vc[at]) * A.vs[r];
-        } else {
-          k[d] = to_f(reinterpret_cast<const T*>(A.kc)[at]);
-          v[d] = to_f(reinterpret_cast<const T*>(A.vc)[at]);
-        }
-        s = fmaf(q[d], k[d], s);
-      }
-      for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-      const float mn = fmaxf(m, s);
-      const float a = m == -INFINITY ? 0.f : __expf(m - mn), p = s == -INFINITY ? 0.f : __expf(s - mn);
-      l = l * a + p;
-      for (int d = 0; d < N; ++d) acc[d] = acc[d] * a + p * v[d];
-      m = mn;
-    };
-    if (!failed) {
-      for (long long j = 0; j < L; ++j) attend(j);
-      if (par)
-        for (int x = t; x >= 0; x = __ldg(par + x)) attend(L + x);
-      else
-        for (int x = 0; x <= t; ++x) attend(L + x);
-    }
-    for (int d = 0; d < N; ++d)
-      reinterpret_cast<T*>(A.out)[o + d * 32 + lane] = from_f<T>(l == 0.f ? 0.f : acc[d] / l);
-    if (A.lse && lane == 0) A.lse[o / D] = l == 0.f ? -INFINITY : m + logf(l);
-  }
+int sm_count_cached() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return -1;
+  static std::atomic<int> cache[64];
+  if (dev < 64 && cache[dev].load() > 0) return cache[dev].load();
+  int n = 0;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return -1;
+  if (dev < 64) cache[dev].store(n);
+  return n;
 }
 
-template <typename T, int D>
-spec_status_t launch(const AttnParams& A, bool e4m3, cudaStream_t s) {
-  const long long rows = (long long)A.T * A.Hq;
-  const long long blocks = (rows + kWarps - 1) / kWarps;
-  const dim3 grid((unsigned)(blocks < 65536 ? blocks : 65536), A.B);
-  if (e4m3)
-    attention_kernel<T, D, true><<<grid, kWarps * 32, 0, s>>>(A);
-  else
-    attention_kernel<T, D, false><<<grid, kWarps * 32, 0, s>>>(A);
-  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled encode_tiled() {
+  static std::atomic<void*> f{nullptr};
+  void* p = f.load();
+  if (!p) {
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    f.store(p);
+  }
+  return reinterpret_cast<EncodeTiled>(p);
+}
+
+// A cache [pages][page_size][H][D] as a 4-dimensional map; a box is one page's rows (at most a tile's) of one
+// head: all of its bytes for codes, 64 elements at a time for 16 bits.
+bool cache_map(CUtensorMap* m, const void* cache, bool e4m3, bool bf16, int D, int H, int page_size, long long pages) {
+  const EncodeTiled f = encode_tiled();
+  if (!f) return false;
+  const cuuint64_t S = e4m3 ? 1 : 2;
+  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)page_size, (cuuint64_t)(pages > 0 ? pages : 1)};
+  const cuuint64_t strides[3] = {D * S, (cuuint64_t)H * D * S, (cuuint64_t)page_size * H * D * S};
+  const cuuint32_t box[4] = {(cuuint32_t)(e4m3 ? D : 64), 1, (cuuint32_t)(page_size < kTile ? page_size : kTile), 1};
+  const cuuint32_t step[4] = {1, 1, 1, 1};
+  return f(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+           const_cast<void*>(cache), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+           e4m3 && D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, e4m3 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
 
 extern "C" size_t spec_attention_workspace_bytes(int T, int num_heads, int num_kv_heads, int head_dim) {
   if (T < 1 || num_heads < 1 || num_kv_heads < 1 || num_heads % num_kv_heads != 0 || (head_dim != 64 && head_dim != 128)) return 0;
-  return 256;
+  return layout((long long)T * (num_heads / num_kv_heads), head_dim).total;
 }
 
 extern "C" spec_status_t spec_attention(const void* q, spec_dtype_t dtype, long long q_stride, int B, int T,
@@ -158,6 +110,9 @@ extern "C" spec_status_t spec_attention(const void* q, spec_dtype_t dtype, long 
   if (head_dim != 64 && head_dim != 128) return SPEC_ERR_UNSUPPORTED;
   if (page_size < 8 || (page_size & (page_size - 1)) != 0 || num_pages > INT_MAX) return SPEC_ERR_UNSUPPORTED;
   if (parents && T > SPEC_MAX_WALK_NODES) return SPEC_ERR_UNSUPPORTED;
+  // a request's rows and positions are counted in 32 bits
+  if ((long long)T * (num_heads / num_kv_heads) > INT_MAX / 2 || (long long)pages_per_request * page_size > INT_MAX / 2)
+    return SPEC_ERR_UNSUPPORTED;
   if (B > 65535) return SPEC_ERR_UNSUPPORTED;
   if (B == 0) return SPEC_OK;
   if (T == 0) {  // no tokens: nothing to check, nothing wrong
@@ -172,10 +127,22 @@ extern "C" spec_status_t spec_attention(const void* q, spec_dtype_t dtype, long 
   if (q_stride < (long long)num_heads * head_dim || q_stride % 8 != 0) return SPEC_ERR_INVALID_ARG;
   if (!workspace || ((uintptr_t)workspace & 255u) || workspace_bytes < spec_attention_workspace_bytes(T, num_heads, num_kv_heads, head_dim))
     return SPEC_ERR_WORKSPACE;
-  AttnParams A = {};
+  const int sms = sm_count_cached();
+  if (sms <= 0) return SPEC_ERR_CUDA;
+  const int G = num_heads / num_kv_heads;
+  const long long rows = (long long)T * G;
+  const int UR = unit_rows(rows);
+  Params A = {};
+  const bool bf16 = dtype == SPEC_DTYPE_BF16;
+  if (!cache_map(&A.kmap, k_cache, e4m3, bf16, head_dim, num_kv_heads, page_size, num_pages) ||
+      !cache_map(&A.vmap, v_cache, e4m3, bf16, head_dim, num_kv_heads, page_size, num_pages))
+    return SPEC_ERR_CUDA;
+  const Layout L = layout(rows, head_dim);
+  unsigned char* w = static_cast<unsigned char*>(workspace);
+  A.part_o = reinterpret_cast<float*>(w + L.o);
+  A.part_ml = reinterpret_cast<float2*>(w + L.ml);
+  A.rec = reinterpret_cast<Record*>(w + L.rec);
   A.q = static_cast<const unsigned char*>(q);
-  A.kc = static_cast<const unsigned char*>(k_cache);
-  A.vc = static_cast<const unsigned char*>(v_cache);
   A.ks = k_scale;
   A.vs = v_scale;
   A.q_stride = q_stride;
@@ -184,18 +151,22 @@ extern "C" spec_status_t spec_attention(const void* q, spec_dtype_t dtype, long 
   A.T = T;
   A.Hq = num_heads;
   A.H = num_kv_heads;
-  A.page_size = page_size;
+  A.G = G;
   A.P = pages_per_request;
+  while ((1 << A.page_log2) < page_size) ++A.page_log2;
+  A.nqp = (int)((rows + UR - 1) / UR);
   A.table = page_table;
   A.context_len = context_len;
   A.chunk_len = chunk_len;
   A.parents = parents;
-  A.scale = scale;
+  A.c = scale * specv::attn::kLog2e;
   A.out = static_cast<unsigned char*>(out);
   A.lse = lse;
   A.err_flags = err_flags;
+  const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (dtype == SPEC_DTYPE_BF16)
-    return head_dim == 64 ? launch<__nv_bfloat16, 64>(A, e4m3, s) : launch<__nv_bfloat16, 128>(A, e4m3, s);
-  return head_dim == 64 ? launch<__half, 64>(A, e4m3, s) : launch<__half, 128>(A, e4m3, s);
+  const bool pair = UR > kTile;
+  const cudaError_t e = bf16 ? specv::attn::launch_attention<__nv_bfloat16>(A, head_dim, e4m3, pair, ctas, s)
+                             : specv::attn::launch_attention<__half>(A, head_dim, e4m3, pair, ctas, s);
+  return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }

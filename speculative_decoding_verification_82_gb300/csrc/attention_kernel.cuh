@@ -1,0 +1,979 @@
+// attention_kernel.cuh -- the attention kernel of spec_attention (sm_103a): tcgen05 products over TMA-loaded
+// pages, one CTA per SM, work split evenly over the SMs along the KV axis.
+//
+// Mathematics.  For a row (token t, query head) with scores s_j = scale q . k_j over the positions j it
+// attends to, the output is sum_j 2^(c s_j - m) v_j / sum_j 2^(c s_j - m), c = log2(e), for any m.  One
+// pass over the tiles keeps a running m, the sum l of the weights in 32 bits and the weighted sum O in
+// 32-bit accumulators; when m has to grow, l and O are multiplied by 2^(m_old - m_new).  m follows the
+// maximum only when that outgrows it by more than 2^8: weights then stay below 2^8, where both
+// 16-bit types and all sums are as exact as below 1, and O is seldom touched.  Two partial results of a
+// row join by the same factor.
+//
+// Rows.  The query heads of one KV head read the same K and V, so the rows of a (request, KV head) are
+// its tokens times its group of heads: row r is token r / G, head r % G.  A tile is 128 rows by 128
+// positions.  Two streams run on each SM, each with its own S and O accumulators in tensor memory and
+// its own softmax warpgroup, so that one stream's softmax overlaps the other's products:
+//   pair  (more than 128 rows): the streams hold two row tiles and share every K and V tile;
+//   split (up to 128 rows): the streams share one row tile and take alternate K and V tiles; their
+//         results join at the end.  Padded rows cost tensor time, which the loads hide: a 128-position
+//         tile of 16-bit K and V takes about 2,800 cycles of an SM's share of HBM, its products 1,024.
+//
+// Work.  The tiles of all (request, row tile, KV head) items in sequence are cut into equal ranges, one
+// per CTA, so ragged lengths and few requests still fill every SM.  Ends of ranges that fall inside an
+// item leave partial results (O, m, l) in the workspace, which attention_combine_kernel joins.
+//
+// Roles.  Warps 0-3 and 4-7: softmax of stream 0 and 1, a thread per row.  Warp 8: one thread issues the
+// products.  Warp 9: TMA loads of K and V pages into a ring of tiles.  Warps 10-11: query rows and
+// tree parents.  Warps 12-15 (e4m3): codes to 16 bits, scaled.  Every wait is bounded: one that gives up
+// sets the CTA's abort flag, every role leaves, copies and products in flight are waited for, and the
+// requests get SPEC_ERRF_TIMEOUT.
+#pragma once
+
+#include <cuda.h>
+#include <math.h>
+
+#include "verify_common.cuh"
+
+namespace specv {
+namespace attn {
+
+constexpr int kTile = 128;       // rows of a row tile, positions of a KV tile
+constexpr int kMaxCtas = 160;    // at most this many CTAs (the workspace's partial results)
+constexpr int kMaxTree = SPEC_MAX_WALK_NODES;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kGrow = 8.f;     // how far (log2) the maximum may outgrow m before O is rescaled
+
+struct Record {  // an item whose tiles several CTAs share: it starts in the CTA that writes the record
+  int b, qp, h;  // b < 0: none
+  int last;      // the last CTA with a part of it
+};
+
+struct Params {
+  CUtensorMap kmap, vmap;
+  const unsigned char* q;
+  const float *ks, *vs;
+  const int32_t *table, *context_len, *chunk_len, *parents;
+  unsigned char* out;
+  float* lse;
+  int32_t* err_flags;
+  float* part_o;   // [2 kMaxCtas][D / 4][unit rows] float4
+  float2* part_ml; // [2 kMaxCtas][unit rows]: m (log2), l
+  Record* rec;     // [kMaxCtas]
+  long long q_stride, num_pages;
+  int B, T, Hq, H, G, P, page_log2;
+  int nqp;         // row units (pair: 256 rows, split: 128) of a request with T tokens
+  float c;         // scale * log2(e)
+};
+
+template <int D, bool E4M3>
+struct Cfg {
+  static constexpr int kHalves = D / 64;               // 64-element (128-byte) column halves of a tile
+  static constexpr int kHalfBytes = kTile * 128;
+  static constexpr int kTileBytes = kHalves * kHalfBytes;
+  static constexpr int kRawBytes = kTile * D;          // a tile of codes
+  static constexpr int kRaw = E4M3 ? (D == 128 ? 4 : 6) : 0;
+  static constexpr int kSlots = E4M3 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 10);
+  static constexpr int kQ = 0;
+  static constexpr int kKv = 2 * kTileBytes;
+  static constexpr int kRawAt = kKv + kSlots * kTileBytes;
+  static constexpr int kMisc = kRawAt + kRaw * kRawBytes;  // parents (pair: 2 KB, split: 512 bytes, then 2 KB of m, l)
+  static constexpr int kBars = kMisc + 2560;
+  static constexpr int kBytes = kBars + 448;
+  static constexpr int kThreads = E4M3 ? 512 : 384;
+  static_assert(kBytes <= 232448, "shared memory");
+};
+
+// ------------------------------------------------------------------------- PTX wrappers ----
+__device__ __forceinline__ void tc_alloc(uint32_t* at) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(at)) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tc_free(uint32_t t) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(t) : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// 32 columns of this warp's 32 lanes.
+__device__ __forceinline__ void tc_ld32(uint32_t t, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(t));
+}
+__device__ __forceinline__ void tc_st32(uint32_t t, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(t)
+      : "memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t t, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(t)
+      : "memory");
+}
+// A box of the 4-dimensional map at (x, y, z, w); x is a multiple of 16 bytes.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+          dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_expect(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ uint4 lds128_at(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+
+// Matrix descriptor: a 128-byte-swizzled tile at `at`.  K-major operands (Q, K): rows of 128 bytes, 8-row
+// groups 1024 bytes apart.  V (positions are its K axis, its D elements contiguous): 64-element columns
+// `lbo` bytes apart, 8-position groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t tile_desc(uint32_t at, uint32_t lbo) {
+  return (uint64_t)((at & 0x3ffffu) >> 4) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+template <typename T>
+struct Half;
+template <>
+struct Half<__nv_bfloat16> {
+  static constexpr uint32_t kFmt = 1;       // tcgen05 operand format
+  static constexpr uint32_t kExp = 0x7f80u; // exponent bits
+  __device__ static uint32_t pack(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+  }
+};
+template <>
+struct Half<__half> {
+  static constexpr uint32_t kFmt = 0;
+  static constexpr uint32_t kExp = 0x7c00u;
+  __device__ static uint32_t pack(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+  }
+};
+// Whether one of the two 16-bit elements is not finite.
+template <typename T>
+__device__ __forceinline__ bool nonfinite2(uint32_t w) {
+  constexpr uint32_t e = Half<T>::kExp;
+  return (w & e) == e || (w & (e << 16)) == (e << 16);
+}
+
+// -------------------------------------------------------------------------- work items ----
+// One request's lengths; bad: they do not fit, and the request has no tiles.
+struct Lens {
+  int L, n;
+  bool bad;
+};
+__device__ __forceinline__ Lens request_lens(const Params& P, int b) {
+  Lens r;
+  r.L = __ldg(P.context_len + b);
+  r.n = P.chunk_len ? __ldg(P.chunk_len + b) : P.T;
+  r.bad = r.L < 0 || r.n < 0 || r.n > P.T || (long long)r.L + r.n > ((long long)P.P << P.page_log2);
+  return r;
+}
+// KV tiles of row unit qp (UR rows): up to its last token in a chain, the whole chunk in a tree.
+template <int UR>
+__device__ __forceinline__ int unit_tiles(const Params& P, const Lens& s, int qp) {
+  const long long rows = (long long)s.n * P.G, r0 = (long long)qp * UR;
+  if (s.bad || r0 >= rows) return 0;
+  const long long r1 = r0 + UR < rows ? r0 + UR : rows;
+  const int last = P.parents ? s.n - 1 : (int)((r1 - 1) / P.G);
+  return (int)(((long long)s.L + last + 1 + kTile - 1) / kTile);
+}
+
+struct Plan {  // a CTA's range
+  long long start, end;      // of the tile sequence
+  long long u_first;         // unit (b, qp) of `start`
+  int h, off;                // its KV head and tile
+};
+
+// A stretch of one item's tiles: offsets [off, off + take) of its tiles counted from the last one.
+struct Seg {
+  int b, qp, h, L, n;
+  int nt, off, take;
+};
+
+template <int UR>
+struct SegIter {
+  long long u, left;
+  int h, off;
+  __device__ SegIter(const Plan& pl) : u(pl.u_first), left(pl.end - pl.start), h(pl.h), off(pl.off) {}
+  __device__ bool next(const Params& P, Seg& s) {
+    if (left <= 0) return false;
+    const long long U = (long long)P.B * P.nqp;
+    for (; u < U; ++u, h = 0, off = 0) {
+      const int b = (int)(u / P.nqp), qp = (int)(u - (long long)b * P.nqp);
+      const Lens r = request_lens(P, b);
+      const int nt = unit_tiles<UR>(P, r, qp);
+      if (nt == 0) continue;
+      s.b = b, s.qp = qp, s.h = h, s.L = r.L, s.n = r.n, s.nt = nt, s.off = off;
+      s.take = (int)(left < nt - off ? left : nt - off);
+      left -= s.take;
+      off = 0;
+      if (++h == P.H) h = 0, ++u;
+      return true;
+    }
+    return false;
+  }
+};
+
+// ------------------------------------------------------------------------------- kernel ----
+template <typename T, int D, bool E4M3, bool PAIR>
+__global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attention_kernel(const __grid_constant__ Params P) {
+  using C = Cfg<D, E4M3>;
+  constexpr int UR = PAIR ? 2 * kTile : kTile;
+  constexpr int NS = C::kSlots, NR = C::kRaw > 0 ? C::kRaw : 1;
+  extern __shared__ __align__(1024) unsigned char smem[];  // (no static shared memory: swizzled tiles start on 1 KB)
+  const uint32_t sbase = smem_addr(smem);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBars);
+  uint64_t* full = bars;               // [NS] a KV tile is in place
+  uint64_t* empty = full + NS;         // [NS] its products are done
+  uint64_t* raw_full = empty + NS;     // [NR] a tile of codes is in place
+  uint64_t* raw_empty = raw_full + NR; // [NR] it has been converted
+  uint64_t* s_full = raw_empty + NR;   // [2] a stream's scores
+  uint64_t* p_ready = s_full + 2;      // [2] its weights (and O rescaled)
+  uint64_t* o_full = p_ready + 2;      // [2] its O is complete
+  uint64_t* q_full = o_full + 2;       // [2] query rows of a segment
+  uint64_t* q_empty = q_full + 2;      // [2]
+  uint64_t* mark = q_empty + 2;        // [4] a masked tile's V has been looked over
+  uint64_t* join = mark + 4;           // [2] split: both streams' m and l are out; both accumulators have been read
+  uint64_t* drain = join + 2;          // [1] after an abort
+  static_assert((2 * NS + 2 * NR + 17) * 8 <= 336, "barriers");
+  uint32_t* words = reinterpret_cast<uint32_t*>(smem + C::kBars + 336);
+  uint32_t* tmem_at = words;                                 // [1]
+  volatile int* abort = reinterpret_cast<int*>(words + 1);   // [1]
+  volatile int* tree_bad = reinterpret_cast<int*>(words + 2);// [2] the request's tree is malformed
+  uint32_t* poison = words + 4;                              // [2 streams][2][4] positions of a tile with a non-finite V
+  Plan& plan = *reinterpret_cast<Plan*>(smem + C::kBars + 416);
+  static_assert(sizeof(Plan) <= 32, "plan");
+  long long* scan = reinterpret_cast<long long*>(smem + C::kMisc);  // [warps], set-up only
+  uint16_t* par = reinterpret_cast<uint16_t*>(smem + C::kMisc);             // pair [kMaxTree], split [2][128]
+  float2* ml = reinterpret_cast<float2*>(smem + C::kMisc + 512);            // split: stream 1's [128], then stream 0's
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  // -- set-up, and this CTA's range of the tile sequence
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(full + i, E4M3 ? kTile : 1);
+      mbar_init(empty + i, 1);
+    }
+    for (int i = 0; i < NR; ++i) {
+      mbar_init(raw_full + i, 1);
+      mbar_init(raw_empty + i, kTile);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s_full + i, 1);
+      mbar_init(p_ready + i, kTile);
+      mbar_init(o_full + i, 1);
+      mbar_init(q_full + i, 64);
+      mbar_init(q_empty + i, 1 + 8);
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(mark + i, kTile);
+    for (int i = 0; i < 2; ++i) mbar_init(join + i, 2 * kTile);
+    mbar_init(drain, 1);
+    fence_mbar_init();
+    *abort = 0;
+    plan.start = plan.end = 0;
+  }
+  if (warp == 8) tc_alloc(tmem_at);
+  {
+    const long long U = (long long)P.B * P.nqp;
+    const long long each = (U + C::kThreads - 1) / C::kThreads;
+    const long long ua = min(U, each * tid), ub = min(U, ua + each);
+    long long sum = 0;
+    for (long long u = ua; u < ub; ++u) {
+      const int b = (int)(u / P.nqp);
+      sum += (long long)unit_tiles<UR>(P, request_lens(P, b), (int)(u - (long long)b * P.nqp)) * P.H;
+    }
+    long long incl = sum;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    long long before = 0, total = 0;
+    for (int w = 0; w < C::kThreads / 32; ++w) {
+      before += w < warp ? scan[w] : 0;
+      total += scan[w];
+    }
+    const long long per = max(1LL, (total + gridDim.x - 1) / gridDim.x);
+    const long long start = min(total, per * blockIdx.x), end = min(total, start + per);
+    if (tid == 0) P.rec[blockIdx.x].b = -1;
+    __syncthreads();  // before the one thread that may write the record
+    long long at = before + incl - sum;
+    const bool has_start = start < end && start >= at && start < at + sum;
+    const bool has_end = start < end && end < total && end >= at && end < at + sum;
+    for (long long u = ua; u < ub && (has_start || has_end); ++u) {
+      const int b = (int)(u / P.nqp), qp = (int)(u - (long long)b * P.nqp);
+      const int nt = unit_tiles<UR>(P, request_lens(P, b), qp);
+      const long long next = at + (long long)nt * P.H;
+      if (has_start && start >= at && start < next) {
+        plan.start = start;
+        plan.end = end;
+        plan.u_first = u;
+        plan.h = (int)((start - at) / nt);
+        plan.off = (int)((start - at) % nt);
+      }
+      if (has_end && end >= at && end < next) {
+        const int h = (int)((end - at) / nt);
+        const long long item = at + (long long)h * nt;
+        if (item >= start && item < end) {  // it starts here and goes on
+          Record r;
+          r.b = b, r.qp = qp, r.h = h;
+          r.last = (int)((item + nt - 1) / per);
+          P.rec[blockIdx.x] = r;
+        }
+      }
+      at = next;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t tmem = *tmem_at;
+  const uint32_t kS[2] = {tmem, tmem + kTile}, kO[2] = {tmem + 2 * kTile, tmem + 3 * kTile};
+
+  // tiles of stream s in a segment
+  auto stream_tiles = [&](const Seg& g, int s) {
+    if (PAIR) return s == 0 || (long long)g.qp * UR + kTile < (long long)g.n * P.G ? g.take : 0;
+    return (g.take + 1 - s) / 2;
+  };
+  bool ok = true;  // no wait gave up
+
+  if (warp < 8) {
+    // ======================================================================= softmax ====
+    if constexpr (E4M3) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    const int s = warp >> 2, row = tid & 127;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
+    const uint32_t S = kS[s] + lanes, O = kO[s] + lanes;
+    if (s == 1) {
+      // requests' flags, and zeros for those whose lengths do not fit
+      for (int b = blockIdx.x; b < P.B; b += gridDim.x) {
+        const Lens r = request_lens(P, b);
+        int flags = r.bad ? SPEC_ERRF_BAD_LENGTH : 0;
+        bool bad = false;
+        if (!r.bad && P.parents)
+          for (int i = row; i < r.n; i += kTile) {
+            const int p = __ldg(P.parents + (size_t)b * P.T + i);
+            bad = bad || (i == 0 ? p != -1 : (p < 0 || p >= i));
+          }
+        int any;
+        asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.or.pred q, 1, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}" : "=r"(any) : "r"((int)bad) : "memory");
+        if (any) flags |= SPEC_ERRF_BAD_TREE;
+        bad = false;
+        if (!flags) {
+          const int pages = (int)(((long long)r.L + r.n + (1LL << P.page_log2) - 1) >> P.page_log2);
+          for (int i = row; i < pages && r.n > 0; i += kTile) {
+            const int p = __ldg(P.table + (size_t)b * P.P + i);
+            bad = bad || p < 0 || p >= P.num_pages;
+          }
+        }
+        asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.or.pred q, 1, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}" : "=r"(any) : "r"((int)bad) : "memory");
+        if (any) flags |= SPEC_ERRF_BAD_SLOT;
+        if (row == 0 && P.err_flags) P.err_flags[b] = flags;
+        if (r.bad) {
+          const size_t rows = (size_t)P.T * P.Hq;
+          uint4* o = reinterpret_cast<uint4*>(P.out + (size_t)b * rows * D * 2);
+          for (size_t i = row; i < rows * D / 8; i += kTile) o[i] = make_uint4(0, 0, 0, 0);
+          if (P.lse)
+            for (size_t i = row; i < rows; i += kTile) P.lse[(size_t)b * rows + i] = -INFINITY;
+        }
+      }
+    }
+    uint32_t ph_s = 0, ph_o = 0, ph_join = 0;  // parities of s_full, o_full, join
+    uint32_t ph_mark[2] = {0, 0};
+    long long kv = 0;             // KV tiles before this segment
+    SegIter<UR> it(plan);
+    Seg g;
+    for (int seg = 0; ok && it.next(P, g); ++seg) {
+      const int cnt = stream_tiles(g, s), cnt1 = s == 1 ? cnt : stream_tiles(g, 1);
+      const int r0 = g.qp * UR + (PAIR ? s * kTile : 0);  // (a unit's rows fit an int: T G <= INT_MAX)
+      const int rows = g.n * P.G;
+      const int r = r0 + row;
+      const bool live = r < rows;
+      const bool warp_live = r0 + (warp & 3) * 32 < rows;
+      const int t = live ? r / P.G : 0;
+      const int qb = PAIR ? 0 : (seg & 1);
+      const uint16_t* pr = par + (PAIR ? 0 : qb * kTile);
+      // positions below `all` are seen by every row of the unit
+      const int all = P.parents ? g.L : g.L + (g.qp * UR) / P.G + 1;
+      const int stop = g.L + g.n;
+      // the segment's first tiles (from the end) are masked
+      if (PAIR && cnt == 0) {  // stream 0 marks them alone
+        const int marked = max(0, min(g.take, g.nt - g.off - all / kTile));
+        ph_mark[0] ^= ((marked + 1) / 2) & 1;
+        ph_mark[1] ^= (marked / 2) & 1;
+      }
+      int node = t;  // tree: the next ancestor to mark
+      float m = -INFINITY, l = 0.f;
+      ok = mbar_wait_warp(q_full + qb, PAIR ? (seg & 1) : ((seg >> 1) & 1), abort);  // parents are in place
+      const bool bad_tree = ok && P.parents && tree_bad[qb];
+      for (int k = 0; ok && k < cnt; ++k) {
+        const int i = PAIR ? k : 2 * k + s;  // the segment's tile
+        const int j0 = (g.nt - 1 - (g.off + i)) * kTile;
+        const bool masked = j0 + kTile > all;
+        ok = mbar_wait_warp(s_full + s, ph_s, abort);
+        ph_s ^= 1;
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};  // the row's positions in this tile
+        if (masked) {
+          // V rows that no one may see become zeros (0 times a NaN is a NaN): those behind the chunk, and
+          // those with a non-finite element, whose readers are marked instead
+          uint64_t* mb = mark + (PAIR ? 0 : 2 * s) + (k & 1);
+          if (!PAIR || s == 0) {
+            const long long seq = 2 * (kv + i) + 1;
+            const int slot = (int)(seq % NS);
+            ok = mbar_wait_warp(full + slot, (uint32_t)((seq / NS) & 1), abort);
+            if (!ok) break;
+            const uint32_t at = sbase + C::kKv + slot * C::kTileBytes + row * 128;
+            const bool hide = j0 + row >= stop;
+            bool nan = false;
+            if (!hide) {
+#pragma unroll
+              for (int x = 0; x < C::kHalves; ++x)
+#pragma unroll
+                for (int y = 0; y < 8; ++y) {
+                  const uint4 v = lds128_at(at + x * C::kHalfBytes + y * 16);
+                  nan = nan || nonfinite2<T>(v.x) || nonfinite2<T>(v.y) || nonfinite2<T>(v.z) || nonfinite2<T>(v.w);
+                }
+            }
+            if (hide || nan) {
+#pragma unroll
+              for (int x = 0; x < C::kHalves; ++x)
+#pragma unroll
+                for (int y = 0; y < 8; ++y) sts128(at + x * C::kHalfBytes + y * 16, 0, 0, 0, 0);
+            }
+            const uint32_t w = __ballot_sync(kFull, nan);
+            if (lane == 0) poison[(PAIR ? 0 : s) * 8 + (k & 1) * 4 + (warp & 3)] = w;
+            __syncwarp();
+            fence_proxy_async_shared();
+            mbar_arrive(mb);
+          }
+          // (two sets of marks suffice: stream 0 meets tile k + 2 only after stream 1's weights of tile k)
+          ok = mbar_wait_warp(mb, ph_mark[k & 1], abort);
+          ph_mark[k & 1] ^= 1;
+          if (!ok) break;
+          // what the row sees: the prefix, then its path
+          const int lim = P.parents ? g.L - j0 : g.L + t + 1 - j0;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const int x = lim - 32 * w;
+            seen[w] = x >= 32 ? ~0u : x <= 0 ? 0u : (1u << x) - 1u;
+          }
+          if (P.parents) {
+            while (node >= 0 && g.L + node >= j0) {
+              const int x = g.L + node - j0;
+              if (x < kTile) {
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+                  if ((x >> 5) == w) seen[w] |= 1u << (x & 31);
+              }
+              const int p = pr[node];
+              node = p == 0xffff ? -1 : p;
+            }
+          }
+          const uint32_t* bad = poison + (PAIR ? 0 : s) * 8 + (k & 1) * 4;
+          if ((bad[0] & seen[0]) | (bad[1] & seen[1]) | (bad[2] & seen[2]) | (bad[3] & seen[3])) l = NAN;
+        }
+        if (warp_live) {
+          uint32_t x[kTile];
+#pragma unroll
+          for (int w = 0; w < 4; ++w) tc_ld32(S + 32 * w, x + 32 * w);
+          tc_wait_ld();
+          if (masked) {
+#pragma unroll
+            for (int j = 0; j < kTile; ++j) x[j] = (seen[j >> 5] >> (j & 31)) & 1u ? x[j] : 0xff800000u;
+          }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int j = 0; j < kTile; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(x[j]));
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * P.c;  // (c > 0; log2 units)
+          const bool grow = top > m + kGrow || (m == -INFINITY && top > m);
+          if (k == 0) {
+            m = top;
+          } else if (__any_sync(kFull, grow)) {
+            float a = 1.f;
+            if (grow) {
+              a = m == -INFINITY ? 0.f : ex2(m - top);
+              m = top;
+              l *= a;
+            }
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w) {
+              uint32_t o[32];
+              tc_ld32(O + 32 * w, o);
+              tc_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * a);
+              tc_st32(O + 32 * w, o);
+            }
+          }
+          const float mm = m == -INFINITY ? 0.f : m;
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            uint32_t p[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float lo = ex2(fmaf(__uint_as_float(x[32 * w + 2 * j]), P.c, -mm));
+              const float hi = ex2(fmaf(__uint_as_float(x[32 * w + 2 * j + 1]), P.c, -mm));
+              sum[(2 * j) & 3] += lo;
+              sum[(2 * j + 1) & 3] += hi;
+              p[j] = Half<T>::pack(lo, hi);  // rounded to the type the product takes
+            }
+            tc_st16(S + 16 * w, p);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tc_wait_st();
+        }
+        tc_fence_before();
+        mbar_arrive(p_ready + s);
+      }
+      // the segment's parents (and, with the products', its queries) may be replaced
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_empty + qb);
+      if (ok && cnt > 0) {
+        ok = mbar_wait_warp(o_full + s, ph_o, abort);
+        ph_o ^= 1;
+        tc_fence_after();
+      }
+      kv += g.take;
+      if (bad_tree) m = -INFINITY, l = 0.f;
+      const bool whole = g.take == g.nt;
+      const int slot = 2 * blockIdx.x + (g.off > 0 ? 0 : 1);
+      const int urow = PAIR ? s * kTile + row : row;  // row of the unit
+      float inv0 = 1.f, inv1 = 0.f;
+      int c0 = 0, c1 = D;
+      bool two = false;
+      if constexpr (!PAIR) {
+        // join the streams: each warpgroup takes half of the columns
+        ml[(1 - s) * kTile + row] = make_float2(m, l);
+        tc_fence_before();
+        mbar_arrive(join);
+        if (ok) ok = mbar_wait_warp(join, ph_join, abort);
+        tc_fence_after();
+        const float2 o = ml[s * kTile + row];
+        const float m0 = s == 0 ? m : o.x, l0 = s == 0 ? l : o.y, m1 = s == 0 ? o.x : m, l1 = s == 0 ? o.y : l;
+        const float M = fmaxf(m0, m1);
+        inv0 = m0 == -INFINITY ? 0.f : ex2(m0 - M);
+        inv1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
+        m = M;
+        l = l0 * inv0 + l1 * inv1;
+        if (!(l0 == l0) || !(l1 == l1)) l = NAN;
+        two = cnt1 > 0;
+        c0 = s * (D / 2);
+        c1 = c0 + D / 2;
+      }
+      const bool work = ok && warp_live && (!PAIR || cnt > 0);
+      if (work) {
+        const float norm = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+        const int hq = g.h * P.G + (r - t * P.G);
+        const size_t orow = live ? ((size_t)g.b * P.T + t) * P.Hq + hq : 0;
+        inv0 *= norm;
+        inv1 *= norm;
+        if (bad_tree) inv0 = inv1 = 0.f;
+        for (int c = c0; c < c1; c += 32) {
+          __syncwarp();
+          uint32_t o[32];
+          tc_ld32(kO[PAIR ? s : 0] + lanes + c, o);
+          tc_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(bad_tree ? 0.f : __uint_as_float(o[j]) * inv0);
+          if (!PAIR && two) {
+            uint32_t o1[32];
+            tc_ld32(kO[1] + lanes + c, o1);
+            tc_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              o[j] = __float_as_uint(bad_tree ? 0.f : fmaf(__uint_as_float(o1[j]), inv1, __uint_as_float(o[j])));
+          }
+          if (whole && !(l == l)) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = 0x7fffffffu;
+          }
+          if (live && whole) {
+            uint4* dst = reinterpret_cast<uint4*>(P.out + (orow * D + c) * 2);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t w[4];
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                w[x] = Half<T>::pack(__uint_as_float(o[8 * j + 2 * x]), __uint_as_float(o[8 * j + 2 * x + 1]));
+              dst[j] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          } else if (live) {
+            float4* dst = reinterpret_cast<float4*>(P.part_o) + ((size_t)slot * (D / 4) + c / 4) * UR + urow;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              dst[(size_t)j * UR] = make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]),
+                                                __uint_as_float(o[4 * j + 2]), __uint_as_float(o[4 * j + 3]));
+          }
+        }
+        if (live && (PAIR || s == 0)) {
+          if (!whole)
+            P.part_ml[(size_t)slot * UR + urow] = make_float2(m, l);
+          else if (P.lse)
+            P.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+        }
+      }
+      if constexpr (!PAIR) {
+        tc_fence_before();
+        mbar_arrive(join + 1);  // both accumulators have been read before either is written again
+        if (ok) ok = mbar_wait_warp(join + 1, ph_join, abort);
+        ph_join ^= 1;
+      }
+    }
+  } else if (warp == 8) {
+    // ====================================================================== products ====
+    if constexpr (E4M3) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (lane == 0) {
+      constexpr uint32_t fmt = Half<T>::kFmt;
+      constexpr uint32_t base = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)(kTile >> 4) << 24);
+      constexpr uint32_t id_qk = base | ((uint32_t)(kTile >> 3) << 17);
+      constexpr uint32_t id_pv = base | (1u << 16) | ((uint32_t)(D >> 3) << 17);  // V: its D axis contiguous
+      uint32_t ph_p[2] = {0, 0};
+      long long kv = 0;
+      SegIter<UR> it(plan);
+      Seg g;
+      for (int seg = 0; ok && it.next(P, g); ++seg) {
+        const int qb = PAIR ? 0 : (seg & 1);
+        const int cnt[2] = {stream_tiles(g, 0), stream_tiles(g, 1)};
+        ok = mbar_wait(q_full + qb, PAIR ? (seg & 1) : ((seg >> 1) & 1), abort);
+        tc_fence_after();
+        // S of stream s from its k-th tile; the last reader of the K tile frees it
+        auto qk = [&](int s, int k) {
+          const long long seq = 2 * (kv + (PAIR ? k : 2 * k + s));
+          const int slot = (int)(seq % NS);
+          ok = ok && mbar_wait(full + slot, (uint32_t)((seq / NS) & 1), abort);
+          if (!ok) return;
+          tc_fence_after();
+          const uint64_t a = tile_desc(sbase + C::kQ + (PAIR ? s : qb) * C::kTileBytes, 16);
+          const uint64_t b = tile_desc(sbase + C::kKv + slot * C::kTileBytes, 16);
+#pragma unroll
+          for (int x = 0; x < D / 16; ++x) {
+            const uint32_t step = ((x / 4) * C::kHalfBytes + (x % 4) * 32) >> 4;
+            tc_mma_ss(kS[s], a + step, b + step, id_qk, x > 0);
+          }
+          tc_commit(s_full + s);
+          if (!PAIR || s == 1 || cnt[1] == 0) tc_commit(empty + slot);
+        };
+        auto pv = [&](int s, int k) {
+          const long long seq = 2 * (kv + (PAIR ? k : 2 * k + s)) + 1;
+          const int slot = (int)(seq % NS);
+          ok = ok && mbar_wait(p_ready + s, ph_p[s], abort);
+          ph_p[s] ^= 1;
+          ok = ok && mbar_wait(full + slot, (uint32_t)((seq / NS) & 1), abort);
+          if (!ok) return;
+          tc_fence_after();
+          const uint64_t b = tile_desc(sbase + C::kKv + slot * C::kTileBytes, C::kHalfBytes);
+#pragma unroll
+          for (int x = 0; x < kTile / 16; ++x) tc_mma_ts(kO[s], kS[s] + 8 * x, b + ((x * 2048) >> 4), id_pv, k > 0 || x > 0);
+          if (!PAIR || s == 1 || cnt[1] == 0) tc_commit(empty + slot);
+          if (k == cnt[s] - 1) tc_commit(o_full + s);
+        };
+        qk(0, 0);
+        if (cnt[1] > 0) qk(1, 0);
+        for (int k = 0; ok && k < cnt[0]; ++k)
+          for (int s = 0; s < 2; ++s) {
+            if (k >= cnt[s]) continue;
+            pv(s, k);
+            if (k + 1 < cnt[s]) qk(s, k + 1);
+          }
+        if (ok) tc_commit(q_empty + qb);
+        kv += g.take;
+      }
+      if (!ok) {  // products in flight end before tensor memory is given back
+        *abort = 1;
+        tc_commit(drain);
+        const long long t0 = clock64();
+        while (!mbar_try_wait(drain, 0) && clock64() - t0 < kWaitLimitCycles) {
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // ========================================================================= loads ====
+    if constexpr (E4M3) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    constexpr int N = E4M3 ? NR : NS;              // the ring that copies land in
+    constexpr int kBoxes = E4M3 ? 1 : C::kHalves;  // column boxes of a row
+    constexpr uint32_t kStage = E4M3 ? C::kRawBytes : C::kTileBytes;
+    uint64_t* fb = E4M3 ? raw_full : full;
+    uint64_t* eb = E4M3 ? raw_empty : empty;
+    const uint32_t ring = sbase + (E4M3 ? C::kRawAt : C::kKv);
+    const int box_log2 = P.page_log2 < 7 ? P.page_log2 : 7;  // rows of a box
+    const int pieces = kTile >> box_log2;
+    const int piece = lane / kBoxes, col = lane % kBoxes;
+    const bool mine = piece < pieces;  // (at most 16 pieces of 2 boxes)
+    long long seq = 0;
+    SegIter<UR> it(plan);
+    Seg g;
+    while (ok && it.next(P, g)) {
+      const int32_t* table = P.table + (size_t)g.b * P.P;
+      const int stop = g.L + g.n;
+      auto page_of = [&](int i) {  // this lane's page in the segment's tile i; -1 reads zeros
+        const int j = (g.nt - 1 - (g.off + i)) * kTile + (piece << box_log2);
+        if (!mine || i >= g.take || j >= stop) return -1;
+        const int p = __ldg(table + (j >> P.page_log2));
+        return p >= 0 && p < P.num_pages ? p : -1;
+      };
+      int page = page_of(0);
+      for (int i = 0; ok && i < g.take; ++i) {
+        const int j = (g.nt - 1 - (g.off + i)) * kTile + (piece << box_log2);
+        const int now = page;
+        page = page_of(i + 1);
+        for (int v = 0; ok && v < 2; ++v, ++seq) {
+          const int slot = (int)(seq % N);
+          if (seq >= N) ok = mbar_wait_warp(eb + slot, (uint32_t)((seq / N - 1) & 1), abort);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect(fb + slot, kStage);
+          __syncwarp();
+          if (mine)
+            tma_load_4d(ring + slot * kStage + col * C::kHalfBytes + ((uint32_t)piece << box_log2) * (E4M3 ? D : 128),
+                        v ? &P.vmap : &P.kmap, col * 64, g.h, j & ((1 << P.page_log2) - 1), now, fb + slot);
+        }
+      }
+    }
+    if (!ok) {  // copies in flight land before the CTA ends
+      *abort = 1;
+      const long long first = seq > N ? seq - N : 0;
+      for (long long x = first; x < seq; ++x) {
+        const long long t0 = clock64();
+        while (!mbar_try_wait(fb + x % N, (uint32_t)((x / N) & 1)) && clock64() - t0 < kWaitLimitCycles) {
+        }
+      }
+    }
+  } else if (warp < 12) {
+    // ======================================================================= queries ====
+    if constexpr (E4M3) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    const int ql = tid - 320;  // 0..63
+    SegIter<UR> it(plan);
+    Seg g;
+    for (int seg = 0; ok && it.next(P, g); ++seg) {
+      const int qb = PAIR ? 0 : (seg & 1), use = PAIR ? seg : seg >> 1;
+      if (use > 0) ok = mbar_wait_warp(q_empty + qb, (uint32_t)((use - 1) & 1), abort);
+      if (!ok) break;
+      const int rows = min(UR, g.n * P.G - g.qp * UR);
+      const unsigned char* q = P.q + ((long long)g.b * P.T * P.q_stride + (long long)g.h * P.G * D) * 2;
+      constexpr int V = D / 8;  // 16-byte vectors of a row
+      for (int i0 = ql; i0 < rows * V; i0 += 64 * 8) {
+        uint4 x[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int i = i0 + u * 64, r = i / V;
+          if (i < rows * V) {
+            const int rr = g.qp * UR + r, t = rr / P.G;
+            x[u] = __ldg(reinterpret_cast<const uint4*>(q + (t * P.q_stride + (long long)(rr - t * P.G) * D) * 2) + i % V);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int i = i0 + u * 64, r = i / V, c = i % V;
+          if (i < rows * V)
+            sts128(sbase + C::kQ + (PAIR ? r / kTile : qb) * C::kTileBytes + (c / 8) * C::kHalfBytes + (r % kTile) * 128 +
+                       (((c % 8) ^ (r & 7)) << 4),
+                   x[u].x, x[u].y, x[u].z, x[u].w);
+        }
+      }
+      if (P.parents && warp == 10) {
+        uint16_t* pr = par + (PAIR ? 0 : qb * kTile);
+        bool bad = false;
+        for (int i = lane; i < g.n; i += 32) {
+          const int p = __ldg(P.parents + (size_t)g.b * P.T + i);
+          const bool fine = i == 0 ? p == -1 : (p >= 0 && p < i);
+          bad = bad || !fine;
+          pr[i] = i > 0 && fine ? (uint16_t)p : (uint16_t)0xffff;
+        }
+        bad = __any_sync(kFull, bad);
+        if (lane == 0) tree_bad[qb] = bad;
+        __syncwarp();
+      }
+      fence_proxy_async_shared();
+      mbar_arrive(q_full + qb);
+    }
+  } else {
+    // ================================================================= codes to 16 bits ====
+    if constexpr (E4M3) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+      const int row = tid - 384;
+      long long seq = 0;
+      SegIter<UR> it(plan);
+      Seg g;
+      while (ok && it.next(P, g)) {
+        const int stop = g.L + g.n;
+        const int32_t* table = P.table + (size_t)g.b * P.P;
+        // the scales of this thread's row in the segment's tile i (0 where there is no row)
+        auto scales_of = [&](int i) {
+          const int j = (g.nt - 1 - (g.off + i)) * kTile + row;
+          if (i >= g.take || j >= stop) return make_float2(0.f, 0.f);
+          const int p = __ldg(table + (j >> P.page_log2));
+          if (p < 0 || p >= P.num_pages) return make_float2(0.f, 0.f);
+          const size_t at = (((size_t)p << P.page_log2) + (j & ((1 << P.page_log2) - 1))) * P.H + g.h;
+          return make_float2(__ldg(P.ks + at), __ldg(P.vs + at));
+        };
+        float2 sc = scales_of(0);
+        for (int i = 0; ok && i < g.take; ++i) {
+          const float2 now = sc;
+          sc = scales_of(i + 1);
+          for (int v = 0; ok && v < 2; ++v, ++seq) {
+            const int rs = (int)(seq % NR), slot = (int)(seq % NS);
+            ok = mbar_wait_warp(raw_full + rs, (uint32_t)((seq / NR) & 1), abort);
+            if (ok && seq >= NS) ok = mbar_wait_warp(empty + slot, (uint32_t)((seq / NS - 1) & 1), abort);
+            if (!ok) break;
+            const float scale = v ? now.y : now.x;
+            const uint32_t src = sbase + C::kRawAt + rs * C::kRawBytes + row * D;
+            const uint32_t dst = sbase + C::kKv + slot * C::kTileBytes + row * 128;
+#pragma unroll
+            for (int y = 0; y < D / 16; ++y) {
+              // the copy's swizzle: 16-byte pieces of a 128-byte row exchanged by its row of 8 (of a
+              // 64-byte row by its pair of rows of 4)
+              const int at = D == 128 ? (y ^ (row & 7)) : (y ^ ((row >> 1) & 3));
+              const uint4 code = lds128_at(src + (at << 4));
+              const uint32_t w[4] = {code.x, code.y, code.z, code.w};
+              uint32_t o[8];
+#pragma unroll
+              for (int z = 0; z < 8; ++z) {
+                uint32_t h;
+                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(w[z >> 1] >> (16 * (z & 1)))));
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+                o[z] = Half<T>::pack(f.x * scale, f.y * scale);
+              }
+              const int h = y / 4, c = 2 * (y % 4);
+              sts128(dst + h * C::kHalfBytes + ((c ^ (row & 7)) << 4), o[0], o[1], o[2], o[3]);
+              sts128(dst + h * C::kHalfBytes + (((c + 1) ^ (row & 7)) << 4), o[4], o[5], o[6], o[7]);
+            }
+            fence_proxy_async_shared();
+            mbar_arrive(full + slot);
+            mbar_arrive(raw_empty + rs);
+          }
+        }
+      }
+    }
+  }
+  if (!ok) *abort = 1;
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tc_free(tmem);
+  }
+  if (*abort && P.err_flags)
+    for (int b = tid; b < P.B; b += C::kThreads) atomicOr(P.err_flags + b, SPEC_ERRF_TIMEOUT);
+}
+
+// Joins the parts of the items that several CTAs share.  Block (c, y): the item that starts in CTA c, 16 of
+// its rows; a thread takes four columns of a row (or fewer rows at a time for 64 columns).
+template <typename T, int D>
+__global__ void __launch_bounds__(256) attention_combine_kernel(const __grid_constant__ Params P, int UR) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c = blockIdx.x;
+  const Record rec = P.rec[c];
+  if (rec.b < 0) return;
+  const int n = P.chunk_len ? __ldg(P.chunk_len + rec.b) : P.T;
+  const int rows = min((long long)UR, (long long)n * P.G - (long long)rec.qp * UR);
+  const int row = blockIdx.y * 16 + (threadIdx.x & 15);
+  if (row >= rows) return;
+  const float2* ml = P.part_ml + row;
+  float M = -INFINITY;
+  for (int x = c; x <= rec.last; ++x) M = fmaxf(M, ml[(size_t)(2 * x + (x == c)) * UR].x);
+  const int r = rec.qp * UR + row, t = r / P.G;
+  const size_t orow = ((size_t)rec.b * P.T + t) * P.Hq + rec.h * P.G + (r - t * P.G);
+  for (int q4 = threadIdx.x >> 4; q4 < D / 4; q4 += 16) {
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int x = c; x <= rec.last; ++x) {
+      const size_t slot = 2 * x + (x == c);
+      const float2 v = ml[slot * UR];
+      const float w = v.x == -INFINITY ? 0.f : ex2(v.x - M);
+      const float4 p = reinterpret_cast<const float4*>(P.part_o)[(slot * (D / 4) + q4) * UR + row];
+      l = v.y == v.y ? fmaf(v.y, w, l) : NAN;
+      o.x = fmaf(p.x, w, o.x);
+      o.y = fmaf(p.y, w, o.y);
+      o.z = fmaf(p.z, w, o.z);
+      o.w = fmaf(p.w, w, o.w);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint2 w2;
+    w2.x = Half<T>::pack(o.x * inv, o.y * inv);
+    w2.y = Half<T>::pack(o.z * inv, o.w * inv);
+    *reinterpret_cast<uint2*>(P.out + (orow * D + 4 * q4) * 2) = w2;
+    if (q4 == 0 && P.lse) P.lse[orow] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
+  }
+}
+
+// Launches both kernels on `stream`.
+template <typename T, int D, bool E4M3, bool PAIR>
+cudaError_t launch_one(const Params& P, int ctas, cudaStream_t stream) {
+  using C = Cfg<D, E4M3>;
+  auto* k = attention_kernel<T, D, E4M3, PAIR>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
+  if (e != cudaSuccess) return e;
+  k<<<ctas, C::kThreads, C::kBytes, stream>>>(P);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  constexpr int UR = PAIR ? 2 * kTile : kTile;
+  const long long rows = (long long)P.T * P.G < UR ? (long long)P.T * P.G : UR;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas, (unsigned)((rows + 15) / 16));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attention_combine_kernel<T, D>, P, UR);
+}
+
+template <typename T>
+cudaError_t launch_attention(const Params& P, int D, bool e4m3, bool pair, int ctas, cudaStream_t stream) {
+  if (D == 64) {
+    if (e4m3) return pair ? launch_one<T, 64, true, true>(P, ctas, stream) : launch_one<T, 64, true, false>(P, ctas, stream);
+    return pair ? launch_one<T, 64, false, true>(P, ctas, stream) : launch_one<T, 64, false, false>(P, ctas, stream);
+  }
+  if (e4m3) return pair ? launch_one<T, 128, true, true>(P, ctas, stream) : launch_one<T, 128, true, false>(P, ctas, stream);
+  return pair ? launch_one<T, 128, false, true>(P, ctas, stream) : launch_one<T, 128, false, false>(P, ctas, stream);
+}
+
+}  // namespace attn
+}  // namespace specv
