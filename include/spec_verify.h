@@ -409,7 +409,9 @@ spec_status_t spec_kv_read(const void *k_cache, const void *v_cache, spec_dtype_
  * whole prefix and, in the chunk, to tokens 0..t (parents NULL) or to itself and its ancestors.
  *   out[b][t][h] = sum_j softmax_j(scale q . k_j) v_j
  * with the scores, the softmax statistics and the sums in 32 bits; the weights are rounded to
- * dtype before they multiply V, and the result is rounded once.
+ * dtype before they multiply V (e4m3 caches: to f16, the V scales taken in; V scales of one request
+ * should lie within 2^-60 .. 2^100, and a bf16 query's elements below 2^-38 of its largest are
+ * rounded to that step), and the result is rounded once.
  *
  * q              token n = b T + t at q + n q_stride (elements; a 16-byte multiple, pointer
  *                16-byte aligned): num_heads rows of head_dim elements, bf16 or f16 (f32:

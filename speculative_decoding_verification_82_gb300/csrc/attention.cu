@@ -86,6 +86,20 @@ bool cache_map(CUtensorMap* m, const void* cache, bool e4m3, bool bf16, int D, i
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The queries [B][T][Hq][D] (tokens q_stride elements apart) as a 4-dimensional map; a box is 64 elements of one
+// KV head's G query heads, for `tokens` tokens.
+bool query_map(CUtensorMap* m, const void* q, bool bf16, int D, int Hq, int G, int T, int B, long long q_stride, int tokens) {
+  const EncodeTiled f = encode_tiled();
+  if (!f || q_stride >= (1LL << 38) / T) return false;  // (strides below 2^40 bytes)
+  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)T, (cuuint64_t)B};
+  const cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)q_stride * 2, (cuuint64_t)T * (cuuint64_t)q_stride * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)G, (cuuint32_t)tokens, 1};
+  const cuuint32_t step[4] = {1, 1, 1, 1};
+  return f(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(q), dims, strides, box,
+           step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
 
 extern "C" size_t spec_attention_workspace_bytes(int T, int num_heads, int num_kv_heads, int head_dim) {
@@ -155,6 +169,15 @@ extern "C" spec_status_t spec_attention(const void* q, spec_dtype_t dtype, long 
   A.P = pages_per_request;
   while ((1 << A.page_log2) < page_size) ++A.page_log2;
   A.nqp = (int)((rows + UR - 1) / UR);
+  if ((long long)B * A.nqp > INT_MAX) return SPEC_ERR_UNSUPPORTED;
+  A.fd_g = specv::make_fastdiv((uint32_t)G);
+  A.fd_nqp = specv::make_fastdiv((uint32_t)A.nqp);
+  // a tile of query rows (64 rows where they all fit) is whole tokens: one box
+  const int qrows = rows <= 64 ? 64 : kTile;
+  if (qrows % G == 0) {
+    const int tokens = qrows / G < T ? qrows / G : T;
+    if (query_map(&A.qmap, q, bf16, head_dim, num_heads, G, T, B, q_stride, tokens)) A.q_box = tokens;
+  }
   A.table = page_table;
   A.context_len = context_len;
   A.chunk_len = chunk_len;

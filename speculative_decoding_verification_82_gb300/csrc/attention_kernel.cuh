@@ -32,6 +32,9 @@
 #include <cuda.h>
 #include <math.h>
 
+#include <type_traits>
+
+#include "fastdiv.h"
 #include "verify_common.cuh"
 
 namespace specv {
@@ -49,7 +52,7 @@ struct Record {  // an item whose tiles several CTAs share: it starts in the CTA
 };
 
 struct Params {
-  CUtensorMap kmap, vmap;
+  CUtensorMap kmap, vmap, qmap;
   const unsigned char* q;
   const float *ks, *vs;
   const int32_t *table, *context_len, *chunk_len, *parents;
@@ -62,25 +65,35 @@ struct Params {
   long long q_stride, num_pages;
   int B, T, Hq, H, G, P, page_log2;
   int nqp;         // row units (pair: 256 rows, split: 128) of a request with T tokens
+  int q_box;       // tokens of qmap's box, 0: query rows are gathered by loads
+  FastDiv fd_g, fd_nqp;
   float c;         // scale * log2(e)
 };
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, bool PAIR>
 struct Cfg {
   static constexpr int kHalves = D / 64;               // 64-element (128-byte) column halves of a tile
   static constexpr int kHalfBytes = kTile * 128;
   static constexpr int kTileBytes = kHalves * kHalfBytes;
   static constexpr int kRawBytes = kTile * D;          // a tile of codes
-  static constexpr int kRaw = E4M3 ? (D == 128 ? 4 : 6) : 0;
-  static constexpr int kSlots = E4M3 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 10);
+  static constexpr int kQTiles = PAIR ? 2 : 1;         // (split: two buffers while 64 rows do, else one)
+  static constexpr int kRaw = E4M3 ? (D == 64 ? 6 : PAIR ? 3 : 4) : 0;
+  static constexpr int kSlots = E4M3 ? (D == 64 ? 6 : PAIR ? 3 : 4) : (D == 64 ? 10 : PAIR ? 5 : 6);
+  // The ring's order is K(0), K(1), V(0), K(2), V(1), ...: a tile's V is wanted a softmax later than its K.
+  // The exponents of a tile's scales are written with its K and kept as long as its softmax is due: until that
+  // frees the V slot, at place p, the ring goes no further than p + kSlots - 1, and up to there lie at most
+  // 1 + ceil((kSlots - 1) / 2) later tiles' K.
+  static constexpr int kScales = E4M3 ? kSlots / 2 + 2 : 0;
   static constexpr int kQ = 0;
-  static constexpr int kKv = 2 * kTileBytes;
+  static constexpr int kKv = kQTiles * kTileBytes;
   static constexpr int kRawAt = kKv + kSlots * kTileBytes;
-  static constexpr int kMisc = kRawAt + kRaw * kRawBytes;  // parents (pair: 2 KB, split: 512 bytes, then 2 KB of m, l)
-  static constexpr int kBars = kMisc + 2560;
+  static constexpr int kParAt = kRawAt + kRaw * kRawBytes;  // parents: 16 bits each (pair), 2 x 128 bytes (split)
+  static constexpr int kScaleAt = kParAt + (PAIR ? 2 * kMaxTree : 2 * kTile);
+  static constexpr int kQexpAt = kScaleAt + kScales * 32;  // exponents of the query rows' scales
+  static constexpr int kBars = kQexpAt + (E4M3 ? 2 * kTile : 0);
   static constexpr int kBytes = kBars + 448;
   static constexpr int kThreads = E4M3 ? 512 : 384;
-  static_assert(kBytes <= 232448, "shared memory");
+  static_assert(kBytes <= 232448 && kBars % 16 == 0, "shared memory");
 };
 
 // ------------------------------------------------------------------------- PTX wrappers ----
@@ -133,6 +146,19 @@ __device__ __forceinline__ void tc_st32(uint32_t t, const uint32_t* r) {
       "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(t)
       : "memory");
 }
+__device__ __forceinline__ void tc_ld16(uint32_t t, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(t));
+}
+__device__ __forceinline__ void tc_st8(uint32_t t, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(t)
+               : "memory");
+}
 __device__ __forceinline__ void tc_st16(uint32_t t, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
@@ -140,6 +166,29 @@ __device__ __forceinline__ void tc_st16(uint32_t t, const uint32_t* r) {
       "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(t)
       : "memory");
+}
+__device__ __forceinline__ void tc_st2(uint32_t t, uint32_t a, uint32_t b) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(t), "r"(a), "r"(b) : "memory");
+}
+__device__ __forceinline__ void tc_ld2(uint32_t t, uint32_t& a, uint32_t& b) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(t));
+}
+// Two 32-bit operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
 }
 // A box of the 4-dimensional map at (x, y, z, w); x is a multiple of 16 bytes.
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar) {
@@ -190,13 +239,6 @@ struct Half<__half> {
     return r;
   }
 };
-// Whether one of the two 16-bit elements is not finite.
-template <typename T>
-__device__ __forceinline__ bool nonfinite2(uint32_t w) {
-  constexpr uint32_t e = Half<T>::kExp;
-  return (w & e) == e || (w & (e << 16)) == (e << 16);
-}
-
 // -------------------------------------------------------------------------- work items ----
 // One request's lengths; bad: they do not fit, and the request has no tiles.
 struct Lens {
@@ -213,17 +255,15 @@ __device__ __forceinline__ Lens request_lens(const Params& P, int b) {
 // KV tiles of row unit qp (UR rows): up to its last token in a chain, the whole chunk in a tree.
 template <int UR>
 __device__ __forceinline__ int unit_tiles(const Params& P, const Lens& s, int qp) {
-  const long long rows = (long long)s.n * P.G, r0 = (long long)qp * UR;
+  const int rows = s.n * P.G, r0 = qp * UR;  // (T G and the positions are at most INT_MAX / 2)
   if (s.bad || r0 >= rows) return 0;
-  const long long r1 = r0 + UR < rows ? r0 + UR : rows;
-  const int last = P.parents ? s.n - 1 : (int)((r1 - 1) / P.G);
-  return (int)(((long long)s.L + last + 1 + kTile - 1) / kTile);
+  const int last = P.parents ? s.n - 1 : (int)fdiv((unsigned)min(r0 + UR, rows) - 1u, P.fd_g);
+  return (s.L + last + kTile) / kTile;
 }
 
-struct Plan {  // a CTA's range
-  long long start, end;      // of the tile sequence
-  long long u_first;         // unit (b, qp) of `start`
-  int h, off;                // its KV head and tile
+struct Plan {  // a CTA's range of the tile sequence
+  long long take;     // its tiles
+  int b, qp, h, off;  // where it starts: item and tile
 };
 
 // A stretch of one item's tiles: offsets [off, off + take) of its tiles counted from the last one.
@@ -234,23 +274,24 @@ struct Seg {
 
 template <int UR>
 struct SegIter {
-  long long u, left;
-  int h, off;
-  __device__ SegIter(const Plan& pl) : u(pl.u_first), left(pl.end - pl.start), h(pl.h), off(pl.off) {}
+  long long left;
+  int b, qp, h, off;
+  __device__ explicit SegIter(const Plan& pl) : left(pl.take), b(pl.b), qp(pl.qp), h(pl.h), off(pl.off) {}
   __device__ bool next(const Params& P, Seg& s) {
     if (left <= 0) return false;
-    const long long U = (long long)P.B * P.nqp;
-    for (; u < U; ++u, h = 0, off = 0) {
-      const int b = (int)(u / P.nqp), qp = (int)(u - (long long)b * P.nqp);
+    while (b < P.B) {
       const Lens r = request_lens(P, b);
       const int nt = unit_tiles<UR>(P, r, qp);
-      if (nt == 0) continue;
-      s.b = b, s.qp = qp, s.h = h, s.L = r.L, s.n = r.n, s.nt = nt, s.off = off;
-      s.take = (int)(left < nt - off ? left : nt - off);
-      left -= s.take;
-      off = 0;
-      if (++h == P.H) h = 0, ++u;
-      return true;
+      if (nt > 0) {
+        s.b = b, s.qp = qp, s.h = h, s.L = r.L, s.n = r.n, s.nt = nt, s.off = off;
+        s.take = (int)(left < nt - off ? left : nt - off);
+        left -= s.take;
+        off = 0;
+        if (++h == P.H) h = 0;
+      }
+      if (nt == 0 || h == 0)
+        if (++qp == P.nqp) qp = 0, ++b;
+      if (nt > 0) return true;
     }
     return false;
   }
@@ -258,8 +299,8 @@ struct SegIter {
 
 // ------------------------------------------------------------------------------- kernel ----
 template <typename T, int D, bool E4M3, bool PAIR>
-__global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attention_kernel(const __grid_constant__ Params P) {
-  using C = Cfg<D, E4M3>;
+__global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_kernel(const __grid_constant__ Params P) {
+  using C = Cfg<D, E4M3, PAIR>;
   constexpr int UR = PAIR ? 2 * kTile : kTile;
   constexpr int NS = C::kSlots, NR = C::kRaw > 0 ? C::kRaw : 1;
   extern __shared__ __align__(1024) unsigned char smem[];  // (no static shared memory: swizzled tiles start on 1 KB)
@@ -276,8 +317,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attention_kernel(co
   uint64_t* q_empty = q_full + 2;      // [2]
   uint64_t* mark = q_empty + 2;        // [4] a masked tile's V has been looked over
   uint64_t* join = mark + 4;           // [2] split: both streams' m and l are out; both accumulators have been read
-  uint64_t* drain = join + 2;          // [1] after an abort
-  static_assert((2 * NS + 2 * NR + 17) * 8 <= 336, "barriers");
+  uint64_t* q_raw = join + 2;          // [1] bf16 queries before they become f16
+  uint64_t* drain = q_raw + 1;         // [1] after an abort
+  static_assert((2 * NS + 2 * NR + 18) * 8 <= 336, "barriers");
   uint32_t* words = reinterpret_cast<uint32_t*>(smem + C::kBars + 336);
   uint32_t* tmem_at = words;                                 // [1]
   volatile int* abort = reinterpret_cast<int*>(words + 1);   // [1]
@@ -285,9 +327,14 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attention_kernel(co
   uint32_t* poison = words + 4;                              // [2 streams][2][4] positions of a tile with a non-finite V
   Plan& plan = *reinterpret_cast<Plan*>(smem + C::kBars + 416);
   static_assert(sizeof(Plan) <= 32, "plan");
-  long long* scan = reinterpret_cast<long long*>(smem + C::kMisc);  // [warps], set-up only
-  uint16_t* par = reinterpret_cast<uint16_t*>(smem + C::kMisc);             // pair [kMaxTree], split [2][128]
-  float2* ml = reinterpret_cast<float2*>(smem + C::kMisc + 512);            // split: stream 1's [128], then stream 0's
+  long long* scan = reinterpret_cast<long long*>(smem + C::kParAt);  // [warps], set-up only
+  using Parent = typename std::conditional<PAIR, uint16_t, uint8_t>::type;   // (split: at most 128 tokens)
+  constexpr Parent kNoParent = (Parent)~(Parent)0;
+  Parent* par = reinterpret_cast<Parent*>(smem + C::kParAt);                // pair [kMaxTree], split [2][128]
+  int* exps = reinterpret_cast<int*>(smem + C::kScaleAt);                   // [kScales][K, V][4]: see the converters
+  uint8_t* qexp = smem + C::kQexpAt;                                        // pair [256], split [2][128]
+  constexpr int ES = C::kScales > 0 ? C::kScales : 1;
+  using OT = typename std::conditional<E4M3, __half, T>::type;              // the products' operands
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   // -- set-up, and this CTA's range of the tile sequence
@@ -309,20 +356,22 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attention_kernel(co
     }
     for (int i = 0; i < 4; ++i) mbar_init(mark + i, kTile);
     for (int i = 0; i < 2; ++i) mbar_init(join + i, 2 * kTile);
+    mbar_init(q_raw, P.q_box > 0 ? 1 : 64);
     mbar_init(drain, 1);
     fence_mbar_init();
     *abort = 0;
-    plan.start = plan.end = 0;
+    plan.take = 0;
   }
   if (warp == 8) tc_alloc(tmem_at);
   {
-    const long long U = (long long)P.B * P.nqp;
-    const long long each = (U + C::kThreads - 1) / C::kThreads;
-    const long long ua = min(U, each * tid), ub = min(U, ua + each);
+    const int U = P.B * P.nqp;  // (at most INT_MAX)
+    const int each = (int)(((unsigned)U + C::kThreads - 1) / C::kThreads);
+    const int ua = (int)min((long long)U, (long long)each * tid), ub = (int)min((long long)U, (long long)ua + each);
+    const int b0 = (int)fdiv((unsigned)ua, P.fd_nqp), qp0 = ua - b0 * P.nqp;
     long long sum = 0;
-    for (long long u = ua; u < ub; ++u) {
-      const int b = (int)(u / P.nqp);
-      sum += (long long)unit_tiles<UR>(P, request_lens(P, b), (int)(u - (long long)b * P.nqp)) * P.H;
+    for (int u = ua, b = b0, qp = qp0; u < ub; ++u) {
+      sum += (long long)unit_tiles<UR>(P, request_lens(P, b), qp) * P.H;
+      if (++qp == P.nqp) qp = 0, ++b;
     }
     long long incl = sum;
     for (int o = 1; o < 32; o <<= 1) {
@@ -330,7 +379,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attention_kernel(co
       if (lane >= o) incl += v;
     }
     if (lane == 31) scan[warp] = incl;
-    __syncthreads();
+    if (tid == 0) P.rec[blockIdx.x].b = -1;
+    __syncthreads();  // (and before the one thread that may write the record)
     long long before = 0, total = 0;
     for (int w = 0; w < C::kThreads / 32; ++w) {
       before += w < warp ? scan[w] : 0;
@@ -338,55 +388,63 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attention_kernel(co
     }
     const long long per = max(1LL, (total + gridDim.x - 1) / gridDim.x);
     const long long start = min(total, per * blockIdx.x), end = min(total, start + per);
-    if (tid == 0) P.rec[blockIdx.x].b = -1;
-    __syncthreads();  // before the one thread that may write the record
     long long at = before + incl - sum;
     const bool has_start = start < end && start >= at && start < at + sum;
     const bool has_end = start < end && end < total && end >= at && end < at + sum;
-    for (long long u = ua; u < ub && (has_start || has_end); ++u) {
-      const int b = (int)(u / P.nqp), qp = (int)(u - (long long)b * P.nqp);
-      const int nt = unit_tiles<UR>(P, request_lens(P, b), qp);
-      const long long next = at + (long long)nt * P.H;
-      if (has_start && start >= at && start < next) {
-        plan.start = start;
-        plan.end = end;
-        plan.u_first = u;
-        plan.h = (int)((start - at) / nt);
-        plan.off = (int)((start - at) % nt);
-      }
-      if (has_end && end >= at && end < next) {
-        const int h = (int)((end - at) / nt);
-        const long long item = at + (long long)h * nt;
-        if (item >= start && item < end) {  // it starts here and goes on
-          Record r;
-          r.b = b, r.qp = qp, r.h = h;
-          r.last = (int)((item + nt - 1) / per);
-          P.rec[blockIdx.x] = r;
+    if (has_start || has_end)
+      for (int u = ua, b = b0, qp = qp0; u < ub; ++u) {
+        const int nt = unit_tiles<UR>(P, request_lens(P, b), qp);
+        const long long next = at + (long long)nt * P.H;
+        if (has_start && start >= at && start < next) {
+          plan.take = end - start;
+          plan.b = b;
+          plan.qp = qp;
+          plan.h = (int)((start - at) / nt);
+          plan.off = (int)((start - at) % nt);
         }
+        if (has_end && end >= at && end < next) {
+          const int h = (int)((end - at) / nt);
+          const long long item = at + (long long)h * nt;
+          if (item >= start && item < end) {  // it starts here and goes on
+            Record r;
+            r.b = b, r.qp = qp, r.h = h;
+            r.last = (int)((item + nt - 1) / per);
+            P.rec[blockIdx.x] = r;
+          }
+        }
+        at = next;
+        if (++qp == P.nqp) qp = 0, ++b;
       }
-      at = next;
-    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = *tmem_at;
-  const uint32_t kS[2] = {tmem, tmem + kTile}, kO[2] = {tmem + 2 * kTile, tmem + 3 * kTile};
+  // tensor memory columns: S of both streams (their weights take its first half), then their O
+  auto col_s = [&](int s) { return tmem + s * kTile; };
+  auto col_o = [&](int s) { return tmem + (2 + s) * kTile; };
 
   // tiles of stream s in a segment
   auto stream_tiles = [&](const Seg& g, int s) {
-    if (PAIR) return s == 0 || (long long)g.qp * UR + kTile < (long long)g.n * P.G ? g.take : 0;
+    if (PAIR) return s == 0 || g.qp * UR + kTile < g.n * P.G ? g.take : 0;
     return (g.take + 1 - s) / 2;
   };
+  // places in the ring, from the segment's first, of the K and V of its tile i
+  auto k_at = [](int i) { return i == 0 ? 0 : 2 * i - 1; };
+  auto v_at = [](const Seg& g, int i) { return i + 1 < g.take ? 2 * i + 2 : 2 * i + 1; };
+  // Query buffers: pair one of two tiles; split two of 64 rows or one of 128 (products read 128 rows of
+  // whatever is there: a row's scores concern that row alone).
+  const int qbufs = !PAIR && P.T * P.G <= 64 ? 2 : 1;
+  const int qhalf = !PAIR && P.T * P.G <= 64 ? C::kHalfBytes / 2 : C::kHalfBytes;  // bytes of a column half
+  const int qbytes = qhalf * C::kHalves;                                           // and of a row tile
   bool ok = true;  // no wait gave up
 
   if (warp < 8) {
     // ======================================================================= softmax ====
-    if constexpr (E4M3) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     const int s = warp >> 2, row = tid & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
-    const uint32_t S = kS[s] + lanes, O = kO[s] + lanes;
+    const uint32_t S = col_s(s) + lanes, O = col_o(s) + lanes;
     if (s == 1) {
       // requests' flags, and zeros for those whose lengths do not fit
       for (int b = blockIdx.x; b < P.B; b += gridDim.x) {
@@ -422,7 +480,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attention_kernel(co
       }
     }
     uint32_t ph_s = 0, ph_o = 0, ph_join = 0;  // parities of s_full, o_full, join
-    uint32_t ph_mark[2] = {0, 0};
+    uint32_t ph_mark = 0;  // bit i: of the marks of tiles k with k & 1 == i
     long long kv = 0;             // KV tiles before this segment
     SegIter<UR> it(plan);
     Seg g;
@@ -433,22 +491,23 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attention_kernel(co
       const int r = r0 + row;
       const bool live = r < rows;
       const bool warp_live = r0 + (warp & 3) * 32 < rows;
-      const int t = live ? r / P.G : 0;
-      const int qb = PAIR ? 0 : (seg & 1);
-      const uint16_t* pr = par + (PAIR ? 0 : qb * kTile);
+      const int t = live ? (int)fdiv((unsigned)r, P.fd_g) : 0;
+      const int qb = seg % qbufs;
+      const Parent* pr = par + (PAIR ? 0 : qb * kTile);
       // positions below `all` are seen by every row of the unit
-      const int all = P.parents ? g.L : g.L + (g.qp * UR) / P.G + 1;
+      const int all = P.parents ? g.L : g.L + (int)fdiv((unsigned)(g.qp * UR), P.fd_g) + 1;
       const int stop = g.L + g.n;
       // the segment's first tiles (from the end) are masked
       if (PAIR && cnt == 0) {  // stream 0 marks them alone
         const int marked = max(0, min(g.take, g.nt - g.off - all / kTile));
-        ph_mark[0] ^= ((marked + 1) / 2) & 1;
-        ph_mark[1] ^= (marked / 2) & 1;
+        ph_mark ^= (((marked + 1) / 2) & 1) | ((marked & 2) ? 2u : 0u);
       }
       int node = t;  // tree: the next ancestor to mark
       float m = -INFINITY, l = 0.f;
-      ok = mbar_wait_warp(q_full + qb, PAIR ? (seg & 1) : ((seg >> 1) & 1), abort);  // parents are in place
+      ok = mbar_wait_warp(q_full + qb, (uint32_t)((seg / qbufs) & 1), abort);  // parents are in place
       const bool bad_tree = ok && P.parents && tree_bad[qb];
+      // e4m3: scores come in units of the row's query scale (a power of two; see the query warps)
+      const int qe = E4M3 && !std::is_same<T, __half>::value ? (int)qexp[PAIR ? s * kTile + row : qb * kTile + row] - 127 : 0;
       for (int k = 0; ok && k < cnt; ++k) {
         const int i = PAIR ? k : 2 * k + s;  // the segment's tile
         const int j0 = (g.nt - 1 - (g.off + i)) * kTile;
@@ -457,28 +516,149 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attention_kernel(co
         ph_s ^= 1;
         if (!ok) break;
         tc_fence_after();
-        uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};  // the row's positions in this tile
+        uint32_t seen[4] = {0, 0, 0, 0};  // a masked tile's positions that the row sees
+        if (masked) {
+          // the prefix, then the row's path
+          const int lim = P.parents ? g.L - j0 : g.L + t + 1 - j0;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const int x = lim - 32 * w;
+            seen[w] = x >= 32 ? ~0u : x <= 0 ? 0u : (1u << x) - 1u;
+          }
+          if (P.parents) {
+            while (node >= 0 && g.L + node >= j0) {
+              const int x = g.L + node - j0;
+              if (x < kTile) {
+                const uint32_t bit = 1u << (x & 31);
+                seen[0] |= x < 32 ? bit : 0u;
+                seen[1] |= (x >> 5) == 1 ? bit : 0u;
+                seen[2] |= (x >> 5) == 2 ? bit : 0u;
+                seen[3] |= (x >> 5) == 3 ? bit : 0u;
+              }
+              const Parent p = pr[node];
+              node = p == kNoParent ? -1 : (int)p;
+            }
+          }
+          // what it does not see becomes -inf in place
+          if (warp_live) {
+#pragma unroll 1
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t bits = w == 0 ? seen[0] : w == 1 ? seen[1] : w == 2 ? seen[2] : seen[3];
+              __syncwarp();
+              if (__all_sync(kFull, bits == ~0u)) continue;
+              uint32_t x[32];
+              tc_ld32(S + 32 * w, x);
+              tc_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) x[j] = bits & (1u << j) ? x[j] : 0xff800000u;
+              tc_st32(S + 32 * w, x);
+            }
+            tc_wait_st();
+          }
+        }
+        if (warp_live) {
+          const int* ke = exps + (int)(E4M3 ? (kv + i) % ES : 0) * 8;  // e4m3: exponents of the tile's scales
+          const int* ve = ke + 4;
+          // scores to log2 units: of positions 32 w on (c > 0)
+          auto factor = [&](int w) {
+            if constexpr (!E4M3) return P.c;
+            return P.c * __uint_as_float((uint32_t)max(1, min(254, qe + ke[w] + 127)) << 23);
+          };
+          // Two passes over the scores, 32 at a time, the next ones on their way: the maximum, then the
+          // weights, which take the place of scores already read.
+          uint32_t x[2][16];
+          float top = -INFINITY;
+          tc_ld16(S, x[0]);
+#pragma unroll
+          for (int w = 0; w < 8; ++w) {
+            tc_wait_ld();
+            tc_ld16(S + (w < 7 ? 16 * (w + 1) : 0), x[(w + 1) & 1]);
+            const uint32_t* y = x[w & 1];
+            float m0 = __uint_as_float(y[0]), m1 = __uint_as_float(y[1]);
+#pragma unroll
+            for (int j = 2; j < 16; j += 2) {
+              m0 = fmaxf(m0, __uint_as_float(y[j]));
+              m1 = fmaxf(m1, __uint_as_float(y[j + 1]));
+            }
+            if constexpr (E4M3)
+              top = fmaxf(top, fmaf(fmaxf(m0, m1), factor(w / 2), (float)ve[w / 2]));
+            else
+              top = fmaxf(top, fmaxf(m0, m1) * P.c);
+          }
+          // f16 weights: 2^7 up, so that they stay below 2^15 after the growth allowed, and only those
+          // below 2^-21 of the largest get subnormal
+          if constexpr (std::is_same<OT, __half>::value) top -= 7.f;
+          if (k == 0) {
+            m = top;
+          } else {
+            const bool grow = top > m + kGrow;
+            if (__any_sync(kFull, grow)) {
+              float a = 1.f;
+              if (grow) {
+                a = m == -INFINITY ? 0.f : ex2(m - top);
+                m = top;
+                l *= a;
+              }
+              tc_wait_ld();
+#pragma unroll 1
+              for (int w = 0; w < D / 32; ++w) {
+                uint32_t o[32];
+                tc_ld32(O + 32 * w, o);
+                tc_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * a);
+                tc_st32(O + 32 * w, o);
+              }
+            }
+          }
+          const float mm = m == -INFINITY ? 0.f : -m;
+#pragma unroll
+          for (int w = 0; w < 8; ++w) {
+            tc_wait_ld();
+            if (w < 7) tc_ld16(S + 16 * (w + 1), x[(w + 1) & 1]);
+            const uint32_t* y = x[w & 1];
+            const float c = factor(w / 2), up = E4M3 ? mm + (float)ve[w / 2] : mm;
+            const float2 c2 = make_float2(c, c), m2 = make_float2(up, up);
+            float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+            uint32_t p[8];
+#pragma unroll
+            for (int j = 0; j < 16; j += 4) {
+              float2 a = fma2(make_float2(__uint_as_float(y[j]), __uint_as_float(y[j + 1])), c2, m2);
+              float2 b = fma2(make_float2(__uint_as_float(y[j + 2]), __uint_as_float(y[j + 3])), c2, m2);
+              a.x = ex2(a.x), a.y = ex2(a.y), b.x = ex2(b.x), b.y = ex2(b.y);
+              s0 = add2(s0, a);
+              s1 = add2(s1, b);
+              p[j / 2] = Half<OT>::pack(a.x, a.y);  // rounded to the type the product takes
+              p[j / 2 + 1] = Half<OT>::pack(b.x, b.y);
+            }
+            tc_st8(S + 8 * w, p);
+            float sum = (s0.x + s0.y) + (s1.x + s1.y);
+            if constexpr (E4M3) sum *= __uint_as_float((uint32_t)(127 - ve[w / 2]) << 23);
+            l += sum;
+          }
+          tc_wait_st();
+        }
         if (masked) {
           // V rows that no one may see become zeros (0 times a NaN is a NaN): those behind the chunk, and
           // those with a non-finite element, whose readers are marked instead
           uint64_t* mb = mark + (PAIR ? 0 : 2 * s) + (k & 1);
           if (!PAIR || s == 0) {
-            const long long seq = 2 * (kv + i) + 1;
+            const long long seq = 2 * kv + v_at(g, i);
             const int slot = (int)(seq % NS);
             ok = mbar_wait_warp(full + slot, (uint32_t)((seq / NS) & 1), abort);
             if (!ok) break;
             const uint32_t at = sbase + C::kKv + slot * C::kTileBytes + row * 128;
             const bool hide = j0 + row >= stop;
-            bool nan = false;
-            if (!hide) {
+            uint32_t bad = 0;  // the top bit of a half is set when its exponent is all ones
 #pragma unroll
-              for (int x = 0; x < C::kHalves; ++x)
+            for (int x = 0; x < C::kHalves; ++x)
 #pragma unroll
-                for (int y = 0; y < 8; ++y) {
-                  const uint4 v = lds128_at(at + x * C::kHalfBytes + y * 16);
-                  nan = nan || nonfinite2<T>(v.x) || nonfinite2<T>(v.y) || nonfinite2<T>(v.z) || nonfinite2<T>(v.w);
-                }
-            }
+              for (int y = 0; y < 8; ++y) {
+                const uint4 v = lds128_at(at + x * C::kHalfBytes + y * 16);
+                constexpr uint32_t E = Half<OT>::kExp * 0x10001u, one = (0x8000u - Half<OT>::kExp) * 0x10001u;
+                bad |= ((v.x & E) + one) | ((v.y & E) + one) | ((v.z & E) + one) | ((v.w & E) + one);
+              }
+            const bool nan = !hide && (bad & 0x80008000u);
             if (hide || nan) {
 #pragma unroll
               for (int x = 0; x < C::kHalves; ++x)
@@ -492,81 +672,11 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attention_kernel(co
             mbar_arrive(mb);
           }
           // (two sets of marks suffice: stream 0 meets tile k + 2 only after stream 1's weights of tile k)
-          ok = mbar_wait_warp(mb, ph_mark[k & 1], abort);
-          ph_mark[k & 1] ^= 1;
+          ok = mbar_wait_warp(mb, (ph_mark >> (k & 1)) & 1, abort);
+          ph_mark ^= 1u << (k & 1);
           if (!ok) break;
-          // what the row sees: the prefix, then its path
-          const int lim = P.parents ? g.L - j0 : g.L + t + 1 - j0;
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const int x = lim - 32 * w;
-            seen[w] = x >= 32 ? ~0u : x <= 0 ? 0u : (1u << x) - 1u;
-          }
-          if (P.parents) {
-            while (node >= 0 && g.L + node >= j0) {
-              const int x = g.L + node - j0;
-              if (x < kTile) {
-#pragma unroll
-                for (int w = 0; w < 4; ++w)
-                  if ((x >> 5) == w) seen[w] |= 1u << (x & 31);
-              }
-              const int p = pr[node];
-              node = p == 0xffff ? -1 : p;
-            }
-          }
           const uint32_t* bad = poison + (PAIR ? 0 : s) * 8 + (k & 1) * 4;
           if ((bad[0] & seen[0]) | (bad[1] & seen[1]) | (bad[2] & seen[2]) | (bad[3] & seen[3])) l = NAN;
-        }
-        if (warp_live) {
-          uint32_t x[kTile];
-#pragma unroll
-          for (int w = 0; w < 4; ++w) tc_ld32(S + 32 * w, x + 32 * w);
-          tc_wait_ld();
-          if (masked) {
-#pragma unroll
-            for (int j = 0; j < kTile; ++j) x[j] = (seen[j >> 5] >> (j & 31)) & 1u ? x[j] : 0xff800000u;
-          }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int j = 0; j < kTile; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(x[j]));
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * P.c;  // (c > 0; log2 units)
-          const bool grow = top > m + kGrow || (m == -INFINITY && top > m);
-          if (k == 0) {
-            m = top;
-          } else if (__any_sync(kFull, grow)) {
-            float a = 1.f;
-            if (grow) {
-              a = m == -INFINITY ? 0.f : ex2(m - top);
-              m = top;
-              l *= a;
-            }
-#pragma unroll
-            for (int w = 0; w < D / 32; ++w) {
-              uint32_t o[32];
-              tc_ld32(O + 32 * w, o);
-              tc_wait_ld();
-#pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * a);
-              tc_st32(O + 32 * w, o);
-            }
-          }
-          const float mm = m == -INFINITY ? 0.f : m;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            uint32_t p[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const float lo = ex2(fmaf(__uint_as_float(x[32 * w + 2 * j]), P.c, -mm));
-              const float hi = ex2(fmaf(__uint_as_float(x[32 * w + 2 * j + 1]), P.c, -mm));
-              sum[(2 * j) & 3] += lo;
-              sum[(2 * j + 1) & 3] += hi;
-              p[j] = Half<T>::pack(lo, hi);  // rounded to the type the product takes
-            }
-            tc_st16(S + 16 * w, p);
-          }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-          tc_wait_st();
         }
         tc_fence_before();
         mbar_arrive(p_ready + s);
@@ -584,71 +694,74 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attention_kernel(co
       const bool whole = g.take == g.nt;
       const int slot = 2 * blockIdx.x + (g.off > 0 ? 0 : 1);
       const int urow = PAIR ? s * kTile + row : row;  // row of the unit
-      float inv0 = 1.f, inv1 = 0.f;
-      int c0 = 0, c1 = D;
+      float f0 = 1.f, f1 = 0.f;                       // factors of the streams' O (pair: of its own)
+      int c0 = 0;
       bool two = false;
       if constexpr (!PAIR) {
         // join the streams: each warpgroup takes half of the columns
-        ml[(1 - s) * kTile + row] = make_float2(m, l);
+        // (m and l go through the streams' S columns, free by now: a warp reads the other's same lanes)
+        __syncwarp();
+        tc_st2(S + kTile - 2, __float_as_uint(m), __float_as_uint(l));
+        tc_wait_st();
         tc_fence_before();
         mbar_arrive(join);
         if (ok) ok = mbar_wait_warp(join, ph_join, abort);
         tc_fence_after();
-        const float2 o = ml[s * kTile + row];
+        uint32_t om, ol;
+        __syncwarp();
+        tc_ld2(col_s(1 - s) + lanes + kTile - 2, om, ol);
+        tc_wait_ld();
+        const float2 o = make_float2(__uint_as_float(om), __uint_as_float(ol));
         const float m0 = s == 0 ? m : o.x, l0 = s == 0 ? l : o.y, m1 = s == 0 ? o.x : m, l1 = s == 0 ? o.y : l;
         const float M = fmaxf(m0, m1);
-        inv0 = m0 == -INFINITY ? 0.f : ex2(m0 - M);
-        inv1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
+        f0 = m0 == -INFINITY ? 0.f : ex2(m0 - M);
+        f1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
         m = M;
-        l = l0 * inv0 + l1 * inv1;
-        if (!(l0 == l0) || !(l1 == l1)) l = NAN;
+        l = l0 * f0 + l1 * f1;  // (a NaN of either stays)
         two = cnt1 > 0;
         c0 = s * (D / 2);
-        c1 = c0 + D / 2;
       }
       const bool work = ok && warp_live && (!PAIR || cnt > 0);
       if (work) {
         const float norm = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-        const int hq = g.h * P.G + (r - t * P.G);
-        const size_t orow = live ? ((size_t)g.b * P.T + t) * P.Hq + hq : 0;
-        inv0 *= norm;
-        inv1 *= norm;
-        if (bad_tree) inv0 = inv1 = 0.f;
-        for (int c = c0; c < c1; c += 32) {
+        f0 *= norm;
+        f1 *= norm;
+        const size_t orow = live ? ((size_t)g.b * P.T + t) * P.Hq + g.h * P.G + (r - t * P.G) : 0;
+        uint4* dst = reinterpret_cast<uint4*>(P.out + (orow * D + c0) * 2);
+        float4* part = reinterpret_cast<float4*>(P.part_o) + ((size_t)slot * (D / 4) + c0 / 4) * UR + urow;
+#pragma unroll 1
+        for (int x = 0; x < (PAIR ? D / 32 : D / 64); ++x, dst += 4, part += 8 * UR) {
           __syncwarp();
           uint32_t o[32];
-          tc_ld32(kO[PAIR ? s : 0] + lanes + c, o);
+          tc_ld32(col_o(PAIR ? s : 0) + lanes + c0 + 32 * x, o);
           tc_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(bad_tree ? 0.f : __uint_as_float(o[j]) * inv0);
+          for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f0);
           if (!PAIR && two) {
             uint32_t o1[32];
-            tc_ld32(kO[1] + lanes + c, o1);
+            tc_ld32(col_o(1) + lanes + c0 + 32 * x, o1);
             tc_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              o[j] = __float_as_uint(bad_tree ? 0.f : fmaf(__uint_as_float(o1[j]), inv1, __uint_as_float(o[j])));
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(fmaf(__uint_as_float(o1[j]), f1, __uint_as_float(o[j])));
           }
-          if (whole && !(l == l)) {
+          if (bad_tree) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = 0x7fffffffu;
+            for (int j = 0; j < 32; ++j) o[j] = 0;
           }
           if (live && whole) {
-            uint4* dst = reinterpret_cast<uint4*>(P.out + (orow * D + c) * 2);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               uint32_t w[4];
 #pragma unroll
-              for (int x = 0; x < 4; ++x)
-                w[x] = Half<T>::pack(__uint_as_float(o[8 * j + 2 * x]), __uint_as_float(o[8 * j + 2 * x + 1]));
+              for (int z = 0; z < 4; ++z)
+                w[z] = Half<T>::pack(__uint_as_float(o[8 * j + 2 * z]), __uint_as_float(o[8 * j + 2 * z + 1]));
               dst[j] = make_uint4(w[0], w[1], w[2], w[3]);
             }
           } else if (live) {
-            float4* dst = reinterpret_cast<float4*>(P.part_o) + ((size_t)slot * (D / 4) + c / 4) * UR + urow;
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-              dst[(size_t)j * UR] = make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]),
-                                                __uint_as_float(o[4 * j + 2]), __uint_as_float(o[4 * j + 3]));
+              part[j * UR] = make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]),
+                                         __uint_as_float(o[4 * j + 2]), __uint_as_float(o[4 * j + 3]));
           }
         }
         if (live && (PAIR || s == 0)) {
@@ -667,60 +780,59 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attention_kernel(co
     }
   } else if (warp == 8) {
     // ====================================================================== products ====
-    if constexpr (E4M3) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (lane == 0) {
-      constexpr uint32_t fmt = Half<T>::kFmt;
+      constexpr uint32_t fmt = Half<OT>::kFmt;
       constexpr uint32_t base = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)(kTile >> 4) << 24);
       constexpr uint32_t id_qk = base | ((uint32_t)(kTile >> 3) << 17);
       constexpr uint32_t id_pv = base | (1u << 16) | ((uint32_t)(D >> 3) << 17);  // V: its D axis contiguous
-      uint32_t ph_p[2] = {0, 0};
+      uint32_t ph_p = 0;  // bit s: p_ready of stream s
       long long kv = 0;
       SegIter<UR> it(plan);
       Seg g;
       for (int seg = 0; ok && it.next(P, g); ++seg) {
-        const int qb = PAIR ? 0 : (seg & 1);
-        const int cnt[2] = {stream_tiles(g, 0), stream_tiles(g, 1)};
-        ok = mbar_wait(q_full + qb, PAIR ? (seg & 1) : ((seg >> 1) & 1), abort);
+        const int qb = seg % qbufs;
+        const int cnt0 = stream_tiles(g, 0), cnt1 = stream_tiles(g, 1);
+        ok = mbar_wait(q_full + qb, (uint32_t)((seg / qbufs) & 1), abort);
         tc_fence_after();
         // S of stream s from its k-th tile; the last reader of the K tile frees it
         auto qk = [&](int s, int k) {
-          const long long seq = 2 * (kv + (PAIR ? k : 2 * k + s));
+          const long long seq = 2 * kv + k_at(PAIR ? k : 2 * k + s);
           const int slot = (int)(seq % NS);
           ok = ok && mbar_wait(full + slot, (uint32_t)((seq / NS) & 1), abort);
           if (!ok) return;
           tc_fence_after();
-          const uint64_t a = tile_desc(sbase + C::kQ + (PAIR ? s : qb) * C::kTileBytes, 16);
+          const uint64_t a = tile_desc(sbase + C::kQ + (PAIR ? s : qb) * qbytes, 16);
           const uint64_t b = tile_desc(sbase + C::kKv + slot * C::kTileBytes, 16);
 #pragma unroll
           for (int x = 0; x < D / 16; ++x) {
-            const uint32_t step = ((x / 4) * C::kHalfBytes + (x % 4) * 32) >> 4;
-            tc_mma_ss(kS[s], a + step, b + step, id_qk, x > 0);
+            tc_mma_ss(col_s(s), a + (((x / 4) * qhalf + (x % 4) * 32) >> 4), b + (((x / 4) * C::kHalfBytes + (x % 4) * 32) >> 4),
+                      id_qk, x > 0);
           }
           tc_commit(s_full + s);
-          if (!PAIR || s == 1 || cnt[1] == 0) tc_commit(empty + slot);
+          if (!PAIR || s == 1 || cnt1 == 0) tc_commit(empty + slot);
         };
         auto pv = [&](int s, int k) {
-          const long long seq = 2 * (kv + (PAIR ? k : 2 * k + s)) + 1;
+          const long long seq = 2 * kv + v_at(g, PAIR ? k : 2 * k + s);
           const int slot = (int)(seq % NS);
-          ok = ok && mbar_wait(p_ready + s, ph_p[s], abort);
-          ph_p[s] ^= 1;
+          ok = ok && mbar_wait(p_ready + s, (ph_p >> s) & 1, abort);
+          ph_p ^= 1u << s;
           ok = ok && mbar_wait(full + slot, (uint32_t)((seq / NS) & 1), abort);
           if (!ok) return;
           tc_fence_after();
           const uint64_t b = tile_desc(sbase + C::kKv + slot * C::kTileBytes, C::kHalfBytes);
 #pragma unroll
-          for (int x = 0; x < kTile / 16; ++x) tc_mma_ts(kO[s], kS[s] + 8 * x, b + ((x * 2048) >> 4), id_pv, k > 0 || x > 0);
-          if (!PAIR || s == 1 || cnt[1] == 0) tc_commit(empty + slot);
-          if (k == cnt[s] - 1) tc_commit(o_full + s);
+          for (int x = 0; x < kTile / 16; ++x) tc_mma_ts(col_o(s), col_s(s) + 8 * x, b + ((x * 2048) >> 4), id_pv, k > 0 || x > 0);
+          if (!PAIR || s == 1 || cnt1 == 0) tc_commit(empty + slot);
+          if (k == (s ? cnt1 : cnt0) - 1) tc_commit(o_full + s);
         };
         qk(0, 0);
-        if (cnt[1] > 0) qk(1, 0);
-        for (int k = 0; ok && k < cnt[0]; ++k)
-          for (int s = 0; s < 2; ++s) {
-            if (k >= cnt[s]) continue;
-            pv(s, k);
-            if (k + 1 < cnt[s]) qk(s, k + 1);
-          }
+        if (cnt1 > 0) qk(1, 0);
+        for (int k = 0; ok && k < cnt0; ++k) {
+          pv(0, k);
+          if (k + 1 < cnt0) qk(0, k + 1);
+          if (k < cnt1) pv(1, k);
+          if (k + 1 < cnt1) qk(1, k + 1);
+        }
         if (ok) tc_commit(q_empty + qb);
         kv += g.take;
       }
@@ -735,7 +847,6 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attention_kernel(co
     __syncwarp();
   } else if (warp == 9) {
     // ========================================================================= loads ====
-    if constexpr (E4M3) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     constexpr int N = E4M3 ? NR : NS;              // the ring that copies land in
     constexpr int kBoxes = E4M3 ? 1 : C::kHalves;  // column boxes of a row
     constexpr uint32_t kStage = E4M3 ? C::kRawBytes : C::kTileBytes;
@@ -758,21 +869,25 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attention_kernel(co
         const int p = __ldg(table + (j >> P.page_log2));
         return p >= 0 && p < P.num_pages ? p : -1;
       };
-      int page = page_of(0);
-      for (int i = 0; ok && i < g.take; ++i) {
+      auto load = [&](bool v, int i, int page) {
         const int j = (g.nt - 1 - (g.off + i)) * kTile + (piece << box_log2);
-        const int now = page;
-        page = page_of(i + 1);
-        for (int v = 0; ok && v < 2; ++v, ++seq) {
-          const int slot = (int)(seq % N);
-          if (seq >= N) ok = mbar_wait_warp(eb + slot, (uint32_t)((seq / N - 1) & 1), abort);
-          if (!ok) break;
-          if (lane == 0) mbar_arrive_expect(fb + slot, kStage);
-          __syncwarp();
-          if (mine)
-            tma_load_4d(ring + slot * kStage + col * C::kHalfBytes + ((uint32_t)piece << box_log2) * (E4M3 ? D : 128),
-                        v ? &P.vmap : &P.kmap, col * 64, g.h, j & ((1 << P.page_log2) - 1), now, fb + slot);
-        }
+        const int slot = (int)(seq % N);
+        if (seq >= N) ok = mbar_wait_warp(eb + slot, (uint32_t)((seq / N - 1) & 1), abort);
+        if (!ok) return;
+        if (lane == 0) mbar_arrive_expect(fb + slot, kStage);
+        __syncwarp();
+        if (mine)
+          tma_load_4d(ring + slot * kStage + col * C::kHalfBytes + ((uint32_t)piece << box_log2) * (E4M3 ? D : 128),
+                      v ? &P.vmap : &P.kmap, col * 64, g.h, j & ((1 << P.page_log2) - 1), page, fb + slot);
+        ++seq;
+      };
+      int was = -1, now = page_of(0), next = page_of(1);
+      for (int i = 0; ok && i <= g.take; ++i) {  // K(i), V(i - 1)
+        if (i < g.take) load(false, i, now);
+        if (ok && i > 0) load(true, i - 1, was);
+        was = now;
+        now = next;
+        next = page_of(i + 2);
       }
     }
     if (!ok) {  // copies in flight land before the CTA ends
@@ -786,98 +901,181 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attention_kernel(co
     }
   } else if (warp < 12) {
     // ======================================================================= queries ====
-    if constexpr (E4M3) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     const int ql = tid - 320;  // 0..63
     SegIter<UR> it(plan);
     Seg g;
     for (int seg = 0; ok && it.next(P, g); ++seg) {
-      const int qb = PAIR ? 0 : (seg & 1), use = PAIR ? seg : seg >> 1;
+      const int qb = seg % qbufs, use = seg / qbufs;
       if (use > 0) ok = mbar_wait_warp(q_empty + qb, (uint32_t)((use - 1) & 1), abort);
       if (!ok) break;
-      const int rows = min(UR, g.n * P.G - g.qp * UR);
-      const unsigned char* q = P.q + ((long long)g.b * P.T * P.q_stride + (long long)g.h * P.G * D) * 2;
+      const int r0 = g.qp * UR, rows = min(UR, g.n * P.G - r0);
       constexpr int V = D / 8;  // 16-byte vectors of a row
-      for (int i0 = ql; i0 < rows * V; i0 += 64 * 8) {
-        uint4 x[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int i = i0 + u * 64, r = i / V;
-          if (i < rows * V) {
-            const int rr = g.qp * UR + r, t = rr / P.G;
-            x[u] = __ldg(reinterpret_cast<const uint4*>(q + (t * P.q_stride + (long long)(rr - t * P.G) * D) * 2) + i % V);
-          }
+      constexpr bool kConvert = E4M3 && !std::is_same<T, __half>::value;  // bf16 to f16
+      const uint32_t qat = sbase + C::kQ + (PAIR ? 0 : qb) * qbytes;
+      uint32_t landing = 0;  // bytes on their way to q_full
+      if (P.q_box > 0) {
+        // whole tokens of G rows fit the tile: boxes of (64 elements, G heads, tokens)
+        const int tiles = PAIR && rows > kTile ? 2 : 1;
+        const uint32_t bytes = (uint32_t)(tiles * C::kHalves * 128 * P.G * P.q_box);
+        if (ql == 0) {
+          uint64_t* bar = kConvert ? q_raw : q_full + qb;
+          mbar_arrive_expect(bar, bytes);
+          const int t0 = (int)fdiv((unsigned)r0, P.fd_g);
+          for (int x = 0; x < tiles; ++x)
+            for (int y = 0; y < C::kHalves; ++y)
+              tma_load_4d(qat + x * qbytes + y * qhalf, &P.qmap, y * 64, g.h * P.G, t0 + x * P.q_box, g.b, bar);
         }
+        if (kConvert) ok = mbar_wait_warp(q_raw, (uint32_t)(seg & 1), abort);
+        landing = bytes;
+      } else {
+        const unsigned char* q = P.q + ((long long)g.b * P.T * P.q_stride + (long long)g.h * P.G * D + ql % V * 8) * 2;
+        constexpr int R = 64 / V;  // rows a pass
+        int r = ql / V;
+        int t = (int)fdiv((unsigned)(r0 + r), P.fd_g), gg = r0 + r - t * P.G;
+        while (r < rows) {
+          uint4 x[8];
+          int n = 0;
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int i = i0 + u * 64, r = i / V, c = i % V;
-          if (i < rows * V)
-            sts128(sbase + C::kQ + (PAIR ? r / kTile : qb) * C::kTileBytes + (c / 8) * C::kHalfBytes + (r % kTile) * 128 +
-                       (((c % 8) ^ (r & 7)) << 4),
-                   x[u].x, x[u].y, x[u].z, x[u].w);
+          for (int u = 0; u < 8; ++u)
+            if (r + u * R < rows) {
+              x[u] = __ldg(reinterpret_cast<const uint4*>(q + (t * P.q_stride + (long long)gg * D) * 2));
+              for (gg += R; gg >= P.G; gg -= P.G) ++t;
+              n = u + 1;
+            }
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            if (u < n) {
+              const int rr = r + u * R, c = ql % V;
+              sts128(qat + (rr / kTile) * qbytes + (c / 8) * qhalf + (rr % kTile) * 128 + (((c % 8) ^ (rr & 7)) << 4), x[u].x,
+                     x[u].y, x[u].z, x[u].w);
+            }
+          r += 8 * R;
+        }
+        if (kConvert) {  // both warps' rows are in place
+          mbar_arrive(q_raw);
+          ok = mbar_wait_warp(q_raw, (uint32_t)(seg & 1), abort);
         }
       }
+      if constexpr (kConvert) {
+        if (!ok) break;
+        // bf16 to f16 in place: a power of two brings the row's largest finite magnitude to 2^14 .. 2^15, so
+        // that only elements below 2^-38 of it lose bits
+        for (int r = ql; r < rows; r += 64) {
+          const uint32_t at = qat + (r / kTile) * qbytes + (r % kTile) * 128;
+          uint32_t top = 0;
+#pragma unroll 4
+          for (int y = 0; y < V; ++y) {
+            const uint4 v = lds128_at(at + (y / 8) * qhalf + (y % 8) * 16);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              const uint32_t lo = (w[z] >> 7) & 0xffu, hi = (w[z] >> 23) & 0xffu;  // exponents
+              top = max(top, max(lo == 255u ? 0u : lo, hi == 255u ? 0u : hi));
+            }
+          }
+          const uint32_t e = max(top, 15u);  // the row in units of 2^(e - 141)
+          const float f = __uint_as_float((268u - e) << 23);
+#pragma unroll 4
+          for (int y = 0; y < V; ++y) {
+            const uint32_t a = at + (y / 8) * qhalf + (y % 8) * 16;
+            const uint4 v = lds128_at(a);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            uint32_t o[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+              o[z] = Half<__half>::pack(__uint_as_float(w[z] << 16) * f, __uint_as_float(w[z] & 0xffff0000u) * f);
+            sts128(a, o[0], o[1], o[2], o[3]);
+          }
+          // the factor back is 2^(e - 141); its float exponent e - 14 is at least 1
+          qexp[PAIR ? r : qb * kTile + r] = (uint8_t)(e - 14);
+        }
+        landing = 0;
+      }
       if (P.parents && warp == 10) {
-        uint16_t* pr = par + (PAIR ? 0 : qb * kTile);
+        Parent* pr = par + (PAIR ? 0 : qb * kTile);
         bool bad = false;
         for (int i = lane; i < g.n; i += 32) {
           const int p = __ldg(P.parents + (size_t)g.b * P.T + i);
           const bool fine = i == 0 ? p == -1 : (p >= 0 && p < i);
           bad = bad || !fine;
-          pr[i] = i > 0 && fine ? (uint16_t)p : (uint16_t)0xffff;
+          pr[i] = i > 0 && fine ? (Parent)p : kNoParent;
         }
         bad = __any_sync(kFull, bad);
         if (lane == 0) tree_bad[qb] = bad;
         __syncwarp();
       }
       fence_proxy_async_shared();
-      mbar_arrive(q_full + qb);
+      if (landing == 0 || ql > 0) mbar_arrive(q_full + qb);  // (thread 0 arrived with its copies)
     }
   } else {
     // ================================================================= codes to 16 bits ====
     if constexpr (E4M3) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
       const int row = tid - 384;
-      long long seq = 0;
+      long long seq = 0, kv = 0;
       SegIter<UR> it(plan);
       Seg g;
       while (ok && it.next(P, g)) {
         const int stop = g.L + g.n;
         const int32_t* table = P.table + (size_t)g.b * P.P;
-        // the scales of this thread's row in the segment's tile i (0 where there is no row)
-        auto scales_of = [&](int i) {
+        // this thread's row of the segment's tile i: its page (-1: none), and its scales
+        auto page_of = [&](int i) {
           const int j = (g.nt - 1 - (g.off + i)) * kTile + row;
-          if (i >= g.take || j >= stop) return make_float2(0.f, 0.f);
-          const int p = __ldg(table + (j >> P.page_log2));
+          return i < g.take && j < stop ? __ldg(table + (j >> P.page_log2)) : -1;
+        };
+        auto scales_of = [&](int i, int p) {
+          const int j = (g.nt - 1 - (g.off + i)) * kTile + row;
           if (p < 0 || p >= P.num_pages) return make_float2(0.f, 0.f);
           const size_t at = (((size_t)p << P.page_log2) + (j & ((1 << P.page_log2) - 1))) * P.H + g.h;
           return make_float2(__ldg(P.ks + at), __ldg(P.vs + at));
         };
-        float2 sc = scales_of(0);
-        for (int i = 0; ok && i < g.take; ++i) {
-          const float2 now = sc;
-          sc = scales_of(i + 1);
-          for (int v = 0; ok && v < 2; ++v, ++seq) {
+        // pages are fetched two tiles ahead, scales one
+        float2 was = make_float2(0.f, 0.f), now = scales_of(0, page_of(0)), next = scales_of(1, page_of(1));
+        int page = page_of(2), ve = 0, ve_next = 0;  // exponents of V(i - 1), V(i)
+        for (int i = 0; ok && i <= g.take; ++i) {  // K(i), V(i - 1)
+          for (int v = i < g.take ? 0 : 1; ok && v < (i > 0 ? 2 : 1); ++v) {
             const int rs = (int)(seq % NR), slot = (int)(seq % NS);
-            ok = mbar_wait_warp(raw_full + rs, (uint32_t)((seq / NR) & 1), abort);
-            if (ok && seq >= NS) ok = mbar_wait_warp(empty + slot, (uint32_t)((seq / NS - 1) & 1), abort);
+            if (seq >= NS) ok = mbar_wait_warp(empty + slot, (uint32_t)((seq / NS - 1) & 1), abort);
+            if (ok) ok = mbar_wait_warp(raw_full + rs, (uint32_t)((seq / NR) & 1), abort);
             if (!ok) break;
-            const float scale = v ? now.y : now.x;
+            // codes to f16, exactly
             const uint32_t src = sbase + C::kRawAt + rs * C::kRawBytes + row * D;
             const uint32_t dst = sbase + C::kKv + slot * C::kTileBytes + row * 128;
+            uint4 code[D / 16];
 #pragma unroll
             for (int y = 0; y < D / 16; ++y) {
               // the copy's swizzle: 16-byte pieces of a 128-byte row exchanged by its row of 8 (of a
               // 64-byte row by its pair of rows of 4)
               const int at = D == 128 ? (y ^ (row & 7)) : (y ^ ((row >> 1) & 3));
-              const uint4 code = lds128_at(src + (at << 4));
-              const uint32_t w[4] = {code.x, code.y, code.z, code.w};
+              code[y] = lds128_at(src + (at << 4));
+            }
+            mbar_arrive(raw_empty + rs);  // (its codes are in registers)
+            // a scale goes with its codes in units of 2^e, e the exponent of the largest finite scale of this
+            // warp's 32 rows (V: within the range that the weights' reference exponent covers)
+            auto exponent = [](float x) {
+              const uint32_t mag = __float_as_uint(fabsf(x));
+              return (int)(__reduce_max_sync(kFull, mag < 0x7f800000u ? mag : 0u) >> 23) - 127;
+            };
+            int e = ve;
+            if (!v) {
+              e = max(-126, exponent(now.x));
+              ve_next = max(-60, min(100, exponent(now.y)));
+              if (lane == 0) {
+                int* at = exps + (int)((kv + i) % ES) * 8 + (warp & 3);
+                at[0] = e;
+                at[4] = ve_next;
+              }
+            }
+            const __half2 rel = __float2half2_rn((v ? was.y : now.x) * __uint_as_float((uint32_t)(127 - e) << 23));
+#pragma unroll
+            for (int y = 0; y < D / 16; ++y) {
+              const uint32_t w[4] = {code[y].x, code[y].y, code[y].z, code[y].w};
               uint32_t o[8];
 #pragma unroll
               for (int z = 0; z < 8; ++z) {
                 uint32_t h;
                 asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(w[z >> 1] >> (16 * (z & 1)))));
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-                o[z] = Half<T>::pack(f.x * scale, f.y * scale);
+                const __half2 f = __hmul2(*reinterpret_cast<const __half2*>(&h), rel);
+                o[z] = *reinterpret_cast<const uint32_t*>(&f);
               }
               const int h = y / 4, c = 2 * (y % 4);
               sts128(dst + h * C::kHalfBytes + ((c ^ (row & 7)) << 4), o[0], o[1], o[2], o[3]);
@@ -885,9 +1083,15 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attention_kernel(co
             }
             fence_proxy_async_shared();
             mbar_arrive(full + slot);
-            mbar_arrive(raw_empty + rs);
+            ++seq;
           }
+          was = now;
+          ve = ve_next;
+          now = next;
+          next = scales_of(i + 2, page);
+          page = page_of(i + 3);
         }
+        kv += g.take;
       }
     }
   }
@@ -945,7 +1149,7 @@ __global__ void __launch_bounds__(256) attention_combine_kernel(const __grid_con
 // Launches both kernels on `stream`.
 template <typename T, int D, bool E4M3, bool PAIR>
 cudaError_t launch_one(const Params& P, int ctas, cudaStream_t stream) {
-  using C = Cfg<D, E4M3>;
+  using C = Cfg<D, E4M3, PAIR>;
   auto* k = attention_kernel<T, D, E4M3, PAIR>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
   if (e != cudaSuccess) return e;

@@ -85,8 +85,8 @@ def sees(T, L, parents=None):
 
 
 def reference(c, b, scale=None):
-    """One request in 64 bits: out [T, Hq, D], the sum of weights times |v|, lse [T, Hq], and the plain sum of
-    |v| over all positions [Hq, D].  Masked values are taken out before the products, so that only attended
+    """One request in 64 bits: out [T, Hq, D], the sum of weights times |v|, lse [T, Hq], and the plain sum over
+    all positions of |v| (e4m3: of |code|, times the request's largest V scale) [Hq, D].  Masked values are taken out before the products, so that only attended
     ones count."""
     B, T, Hq, D = c["q"].shape
     page, H = c["k_cache"].shape[1:3]
@@ -117,7 +117,11 @@ def reference(c, b, scale=None):
         p = torch.softmax(s, -1)
         v = kv[1][:, h]
         fin = torch.isfinite(v)
-        flat[hs] = torch.where(fin, v, torch.zeros_like(v)).abs().sum(0)
+        w = torch.where(fin, v, torch.zeros_like(v)).abs()
+        if c.get("v_scale") is not None:
+            vs = c["v_scale"].view(-1, H)[slot][:, h].double()[:, None]
+            w = w / vs * vs.max()
+        flat[hs] = w.sum(0)
         out[:, hs] = torch.einsum("gtn,nd->tgd", p, torch.where(fin, v, torch.zeros_like(v)))
         mag[:, hs] = torch.einsum("gtn,nd->tgd", p, torch.where(fin, v, torch.zeros_like(v)).abs())
     return out, mag, lse, flat
@@ -137,11 +141,13 @@ def check(c, r, rows=None, scale=None):
         out, mag, lse, flat = reference(c, b, scale)
         got = r["out"][b, :n].double()
         tol = u * (1 + u) * out.abs() + (u + 2.0**-13) * mag + float(torch.finfo(dtype).smallest_normal) * (u + 2.0**-13)
-        if dtype == torch.float16:
-            # a weight below fp16's normals is off by up to half its smallest step, 2^-25, whatever its size; the
-            # weights are relative to one that is at least 1, so their sum is too, and dividing by it only shrinks
-            # the error: at most 2^-25 of the plain sum of |v|
-            tol = tol + 2.0**-25 * flat
+        if dtype == torch.float16 or c.get("v_scale") is not None:
+            # Weights are f16 here (times the V scale of an e4m3 cache: w s), below its normals off by up to half
+            # its smallest step, 2^-25, whatever their size.  They are in units of 2^(M - 7) S, M the row's
+            # largest score and S at most twice the largest V scale (1 without scales), so the largest weight is
+            # at least 2^7 / S and their sum too: dividing by it leaves at most 2^-25 S / 2^7 of the plain sum
+            # of |v| (|code|): 2^-31 of `flat` (half of that without scales).
+            tol = tol + 2.0**-31 * flat
         bad = (got - out).abs() > tol
         if rows is not None:
             keep = torch.zeros(n, dtype=torch.bool, device="cuda")
