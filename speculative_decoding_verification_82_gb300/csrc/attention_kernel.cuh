@@ -22,11 +22,12 @@
 // per CTA, so ragged lengths and few requests still fill every SM.  Ends of ranges that fall inside an
 // item leave partial results (O, m, l) in the workspace, which attention_combine_kernel joins.
 //
-// Roles.  Warps 0-3 and 4-7: softmax of stream 0 and 1, a thread per row.  Warp 8: one thread issues the
-// products.  Warp 9: TMA loads of K and V pages into a ring of tiles.  Warps 10-11: query rows and
-// tree parents.  Warps 12-15 (e4m3): codes to 16 bits, scaled.  Every wait is bounded: one that gives up
-// sets the CTA's abort flag, every role leaves, copies and products in flight are waited for, and the
-// requests get SPEC_ERRF_TIMEOUT.
+// Roles.  Warps 0-3 and 4-7: softmax of stream 0 and 1, a thread per row.  Warp 8: one lane issues the
+// products of both streams in turn (the tensor cores run them in that order, which the places that scores
+// and weights share rely on).  Warp 9: TMA loads of K and V pages into a ring of tiles.  Warp 10: query
+// rows and tree parents.  Warps 11-14 and 15-18 (e4m3): K and V codes to 16 bits.  Every wait is bounded:
+// one that gives up sets the CTA's abort flag, every role leaves, copies and products in flight are waited
+// for, and the requests get SPEC_ERRF_TIMEOUT.
 #pragma once
 
 #include <cuda.h>
@@ -80,20 +81,23 @@ struct Cfg {
   static constexpr int kRaw = E4M3 ? (D == 64 ? 6 : PAIR ? 3 : 4) : 0;
   static constexpr int kSlots = E4M3 ? (D == 64 ? 6 : PAIR ? 3 : 4) : (D == 64 ? 10 : PAIR ? 5 : 6);
   // The ring's order is K(0), K(1), V(0), K(2), V(1), ...: a tile's V is wanted a softmax later than its K.
-  // The exponents of a tile's scales are written with its K and kept as long as its softmax is due: until that
-  // frees the V slot, at place p, the ring goes no further than p + kSlots - 1, and up to there lie at most
-  // 1 + ceil((kSlots - 1) / 2) later tiles' K.
-  static constexpr int kScales = E4M3 ? kSlots / 2 + 2 : 0;
+  // The exponents of a tile's scales are written with its K and kept as long as its softmax is due.  The streams
+  // may drift apart, but by no more than the raw ring is long: its copies are in sequence, and one whose slot is
+  // taken stops it.  So no tile 8 or more ahead is converted meanwhile.
+  static constexpr int kScales = E4M3 ? 8 : 0;
   static constexpr int kQ = 0;
   static constexpr int kKv = kQTiles * kTileBytes;
   static constexpr int kRawAt = kKv + kSlots * kTileBytes;
   static constexpr int kParAt = kRawAt + kRaw * kRawBytes;  // parents: 16 bits each (pair), 2 x 128 bytes (split)
   static constexpr int kScaleAt = kParAt + (PAIR ? 2 * kMaxTree : 2 * kTile);
   static constexpr int kQexpAt = kScaleAt + kScales * 32;  // exponents of the query rows' scales
-  static constexpr int kBars = kQexpAt + (E4M3 ? 2 * kTile : 0);
-  static constexpr int kBytes = kBars + 448;
-  static constexpr int kThreads = E4M3 ? 512 : 384;
+  static constexpr int kMlAt = kQexpAt + (E4M3 ? 2 * kTile : 0);          // split: a float2 a row
+  static constexpr int kBars = kMlAt + (PAIR ? 0 : kTile * 8);
+  static constexpr int kBytes = kBars + 560;
+  static constexpr int kConvert = 11;                      // the first of the warps that convert codes (8 of them)
+  static constexpr int kThreads = (kConvert + (E4M3 ? 8 : 0)) * 32;
   static_assert(kBytes <= 232448 && kBars % 16 == 0, "shared memory");
+  static_assert(kRaw <= kSlots, "see the converters");
 };
 
 // ------------------------------------------------------------------------- PTX wrappers ----
@@ -167,12 +171,6 @@ __device__ __forceinline__ void tc_st16(uint32_t t, const uint32_t* r) {
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(t)
       : "memory");
 }
-__device__ __forceinline__ void tc_st2(uint32_t t, uint32_t a, uint32_t b) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(t), "r"(a), "r"(b) : "memory");
-}
-__device__ __forceinline__ void tc_ld2(uint32_t t, uint32_t& a, uint32_t& b) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(t));
-}
 // Two 32-bit operations in one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 r;
@@ -200,6 +198,17 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
 }
 __device__ __forceinline__ void mbar_arrive_expect(uint64_t* bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes) : "memory");
+}
+// True for one lane of the (whole) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+// One arrival for a warp, after what each of its lanes did (and fenced) before.
+__device__ __forceinline__ void mbar_arrive_warp(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 __device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
@@ -315,17 +324,17 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
   uint64_t* o_full = p_ready + 2;      // [2] its O is complete
   uint64_t* q_full = o_full + 2;       // [2] query rows of a segment
   uint64_t* q_empty = q_full + 2;      // [2]
-  uint64_t* mark = q_empty + 2;        // [4] a masked tile's V has been looked over
-  uint64_t* join = mark + 4;           // [2] split: both streams' m and l are out; both accumulators have been read
-  uint64_t* q_raw = join + 2;          // [1] bf16 queries before they become f16
+  uint64_t* mark = q_empty + 2;        // [8] a masked tile's V has been looked over
+  uint64_t* join = mark + 8;           // [3] split: m and l of stream 1; the factors; both O have been read
+  uint64_t* q_raw = join + 3;          // [1] bf16 queries before they become f16
   uint64_t* drain = q_raw + 1;         // [1] after an abort
-  static_assert((2 * NS + 2 * NR + 18) * 8 <= 336, "barriers");
-  uint32_t* words = reinterpret_cast<uint32_t*>(smem + C::kBars + 336);
+  static_assert((2 * NS + 2 * NR + 23) * 8 <= 384, "barriers");
+  uint32_t* words = reinterpret_cast<uint32_t*>(smem + C::kBars + 384);
   uint32_t* tmem_at = words;                                 // [1]
   volatile int* abort = reinterpret_cast<int*>(words + 1);   // [1]
   volatile int* tree_bad = reinterpret_cast<int*>(words + 2);// [2] the request's tree is malformed
-  uint32_t* poison = words + 4;                              // [2 streams][2][4] positions of a tile with a non-finite V
-  Plan& plan = *reinterpret_cast<Plan*>(smem + C::kBars + 416);
+  uint32_t* poison = words + 4;                              // [8][4] positions of a tile with a non-finite V
+  Plan& plan = *reinterpret_cast<Plan*>(smem + C::kBars + 528);
   static_assert(sizeof(Plan) <= 32, "plan");
   long long* scan = reinterpret_cast<long long*>(smem + C::kParAt);  // [warps], set-up only
   using Parent = typename std::conditional<PAIR, uint16_t, uint8_t>::type;   // (split: at most 128 tokens)
@@ -340,23 +349,23 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
   // -- set-up, and this CTA's range of the tile sequence
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
-      mbar_init(full + i, E4M3 ? kTile : 1);
+      mbar_init(full + i, E4M3 ? 4 : 1);
       mbar_init(empty + i, 1);
     }
     for (int i = 0; i < NR; ++i) {
       mbar_init(raw_full + i, 1);
-      mbar_init(raw_empty + i, kTile);
+      mbar_init(raw_empty + i, 4);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full + i, 1);
-      mbar_init(p_ready + i, kTile);
+      mbar_init(p_ready + i, 4);
       mbar_init(o_full + i, 1);
-      mbar_init(q_full + i, 64);
+      mbar_init(q_full + i, 32);
       mbar_init(q_empty + i, 1 + 8);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(mark + i, kTile);
-    for (int i = 0; i < 2; ++i) mbar_init(join + i, 2 * kTile);
-    mbar_init(q_raw, P.q_box > 0 ? 1 : 64);
+    for (int i = 0; i < 8; ++i) mbar_init(mark + i, 4);
+    for (int i = 0; i < 3; ++i) mbar_init(join + i, i == 1 ? 4 : 8);
+    mbar_init(q_raw, 1);
     mbar_init(drain, 1);
     fence_mbar_init();
     *abort = 0;
@@ -480,8 +489,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
       }
     }
     uint32_t ph_s = 0, ph_o = 0, ph_join = 0;  // parities of s_full, o_full, join
-    uint32_t ph_mark = 0;  // bit i: of the marks of tiles k with k & 1 == i
-    long long kv = 0;             // KV tiles before this segment
+    uint32_t ph_mark = 0;  // bit i: parity of mark[i]
+    uint32_t kv = 0;              // KV tiles before this segment
     SegIter<UR> it(plan);
     Seg g;
     for (int seg = 0; ok && it.next(P, g); ++seg) {
@@ -500,7 +509,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
       // the segment's first tiles (from the end) are masked
       if (PAIR && cnt == 0) {  // stream 0 marks them alone
         const int marked = max(0, min(g.take, g.nt - g.off - all / kTile));
-        ph_mark ^= (((marked + 1) / 2) & 1) | ((marked & 2) ? 2u : 0u);
+        for (int k = 0; k < marked; ++k) ph_mark ^= 1u << (k & 7);
       }
       int node = t;  // tree: the next ancestor to mark
       float m = -INFINITY, l = 0.f;
@@ -557,8 +566,14 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
           }
         }
         if (warp_live) {
-          const int* ke = exps + (int)(E4M3 ? (kv + i) % ES : 0) * 8;  // e4m3: exponents of the tile's scales
-          const int* ve = ke + 4;
+          // e4m3: exponents of the tile's scales, by 32 positions
+          int4 ke4 = make_int4(0, 0, 0, 0), ve4 = ke4;
+          if constexpr (E4M3) {
+            const int4* at = reinterpret_cast<const int4*>(exps + (kv + i) % ES * 8);
+            ke4 = at[0];
+            ve4 = at[1];
+          }
+          const int ke[4] = {ke4.x, ke4.y, ke4.z, ke4.w}, ve[4] = {ve4.x, ve4.y, ve4.z, ve4.w};
           // scores to log2 units: of positions 32 w on (c > 0)
           auto factor = [&](int w) {
             if constexpr (!E4M3) return P.c;
@@ -641,11 +656,13 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
         if (masked) {
           // V rows that no one may see become zeros (0 times a NaN is a NaN): those behind the chunk, and
           // those with a non-finite element, whose readers are marked instead
-          uint64_t* mb = mark + (PAIR ? 0 : 2 * s) + (k & 1);
+          // The streams may be several tiles apart (pair: by fewer than 8, since the ring's tiles are freed by
+          // both), so marks take turns.
+          const int mi = PAIR ? k & 7 : 4 * s + (k & 3);
+          uint64_t* mb = mark + mi;
           if (!PAIR || s == 0) {
-            const long long seq = 2 * kv + v_at(g, i);
-            const int slot = (int)(seq % NS);
-            ok = mbar_wait_warp(full + slot, (uint32_t)((seq / NS) & 1), abort);
+            const uint32_t seq = 2 * kv + v_at(g, i), slot = seq % NS;
+            ok = mbar_wait_warp(full + slot, (seq / NS) & 1, abort);
             if (!ok) break;
             const uint32_t at = sbase + C::kKv + slot * C::kTileBytes + row * 128;
             const bool hide = j0 + row >= stop;
@@ -666,24 +683,21 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
                 for (int y = 0; y < 8; ++y) sts128(at + x * C::kHalfBytes + y * 16, 0, 0, 0, 0);
             }
             const uint32_t w = __ballot_sync(kFull, nan);
-            if (lane == 0) poison[(PAIR ? 0 : s) * 8 + (k & 1) * 4 + (warp & 3)] = w;
-            __syncwarp();
+            if (lane == 0) poison[mi * 4 + (warp & 3)] = w;
             fence_proxy_async_shared();
-            mbar_arrive(mb);
+            mbar_arrive_warp(mb);
           }
-          // (two sets of marks suffice: stream 0 meets tile k + 2 only after stream 1's weights of tile k)
-          ok = mbar_wait_warp(mb, (ph_mark >> (k & 1)) & 1, abort);
-          ph_mark ^= 1u << (k & 1);
+          ok = mbar_wait_warp(mb, (ph_mark >> mi) & 1, abort);
+          ph_mark ^= 1u << mi;
           if (!ok) break;
-          const uint32_t* bad = poison + (PAIR ? 0 : s) * 8 + (k & 1) * 4;
+          const uint32_t* bad = poison + mi * 4;
           if ((bad[0] & seen[0]) | (bad[1] & seen[1]) | (bad[2] & seen[2]) | (bad[3] & seen[3])) l = NAN;
         }
         tc_fence_before();
-        mbar_arrive(p_ready + s);
+        mbar_arrive_warp(p_ready + s);
       }
       // the segment's parents (and, with the products', its queries) may be replaced
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_empty + qb);
+      mbar_arrive_warp(q_empty + qb);
       if (ok && cnt > 0) {
         ok = mbar_wait_warp(o_full + s, ph_o, abort);
         ph_o ^= 1;
@@ -698,34 +712,39 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
       int c0 = 0;
       bool two = false;
       if constexpr (!PAIR) {
-        // join the streams: each warpgroup takes half of the columns
-        // (m and l go through the streams' S columns, free by now: a warp reads the other's same lanes)
-        __syncwarp();
-        tc_st2(S + kTile - 2, __float_as_uint(m), __float_as_uint(l));
-        tc_wait_st();
+        // Join the streams: the first warpgroup makes the factors of both, each takes half of the columns.  (Not
+        // through tensor memory: the next item's scores are on their way to S.)
+        float2* ml = reinterpret_cast<float2*>(smem + C::kMlAt) + row;
+        if (s == 1) *ml = make_float2(m, l);
         tc_fence_before();
-        mbar_arrive(join);
+        mbar_arrive_warp(join);
         if (ok) ok = mbar_wait_warp(join, ph_join, abort);
+        if (s == 0) {
+          const float2 o = *ml;
+          const float M = fmaxf(m, o.x);
+          f0 = m == -INFINITY ? 0.f : ex2(m - M);
+          f1 = o.x == -INFINITY ? 0.f : ex2(o.x - M);
+          l = l * f0 + o.y * f1;  // (a NaN of either stays)
+          m = M;
+          const float norm = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+          f0 *= norm;
+          f1 *= norm;
+          *ml = make_float2(f0, f1);
+          mbar_arrive_warp(join + 1);
+        } else {
+          if (ok) ok = mbar_wait_warp(join + 1, ph_join, abort);
+          const float2 o = *ml;
+          f0 = o.x;
+          f1 = o.y;
+        }
         tc_fence_after();
-        uint32_t om, ol;
-        __syncwarp();
-        tc_ld2(col_s(1 - s) + lanes + kTile - 2, om, ol);
-        tc_wait_ld();
-        const float2 o = make_float2(__uint_as_float(om), __uint_as_float(ol));
-        const float m0 = s == 0 ? m : o.x, l0 = s == 0 ? l : o.y, m1 = s == 0 ? o.x : m, l1 = s == 0 ? o.y : l;
-        const float M = fmaxf(m0, m1);
-        f0 = m0 == -INFINITY ? 0.f : ex2(m0 - M);
-        f1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
-        m = M;
-        l = l0 * f0 + l1 * f1;  // (a NaN of either stays)
         two = cnt1 > 0;
         c0 = s * (D / 2);
+      } else {
+        f0 = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
       }
       const bool work = ok && warp_live && (!PAIR || cnt > 0);
       if (work) {
-        const float norm = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-        f0 *= norm;
-        f1 *= norm;
         const size_t orow = live ? ((size_t)g.b * P.T + t) * P.Hq + g.h * P.G + (r - t * P.G) : 0;
         uint4* dst = reinterpret_cast<uint4*>(P.out + (orow * D + c0) * 2);
         float4* part = reinterpret_cast<float4*>(P.part_o) + ((size_t)slot * (D / 4) + c0 / 4) * UR + urow;
@@ -773,78 +792,95 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
       }
       if constexpr (!PAIR) {
         tc_fence_before();
-        mbar_arrive(join + 1);  // both accumulators have been read before either is written again
-        if (ok) ok = mbar_wait_warp(join + 1, ph_join, abort);
+        mbar_arrive_warp(join + 2);  // both accumulators have been read before either is written again
+        if (ok) ok = mbar_wait_warp(join + 2, ph_join, abort);
         ph_join ^= 1;
       }
     }
   } else if (warp == 8) {
     // ====================================================================== products ====
-    if (lane == 0) {
-      constexpr uint32_t fmt = Half<OT>::kFmt;
-      constexpr uint32_t base = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)(kTile >> 4) << 24);
-      constexpr uint32_t id_qk = base | ((uint32_t)(kTile >> 3) << 17);
-      constexpr uint32_t id_pv = base | (1u << 16) | ((uint32_t)(D >> 3) << 17);  // V: its D axis contiguous
-      uint32_t ph_p = 0;  // bit s: p_ready of stream s
-      long long kv = 0;
-      SegIter<UR> it(plan);
-      Seg g;
-      for (int seg = 0; ok && it.next(P, g); ++seg) {
-        const int qb = seg % qbufs;
-        const int cnt0 = stream_tiles(g, 0), cnt1 = stream_tiles(g, 1);
-        ok = mbar_wait(q_full + qb, (uint32_t)((seg / qbufs) & 1), abort);
+    // (the warp stays together, so that addresses and descriptors are uniform; one lane issues)
+    constexpr uint32_t fmt = Half<OT>::kFmt;
+    constexpr uint32_t base = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)(kTile >> 4) << 24);
+    constexpr uint32_t id_qk = base | ((uint32_t)(kTile >> 3) << 17);
+    constexpr uint32_t id_pv = base | (1u << 16) | ((uint32_t)(D >> 3) << 17);  // V: its D axis contiguous
+    const bool lead = elect_one();
+    uint32_t ph_p = 0;  // bit s: p_ready of stream s
+    uint32_t kv = 0;
+    SegIter<UR> it(plan);
+    Seg g;
+    for (int seg = 0; ok && it.next(P, g); ++seg) {
+      const int qb = seg % qbufs;
+      const int cnt0 = stream_tiles(g, 0), cnt1 = stream_tiles(g, 1);
+      ok = mbar_wait_warp(q_full + qb, (uint32_t)((seg / qbufs) & 1), abort);
+      // S of stream s; the last reader of the K tile frees it
+      auto mma_qk = [&](int s, uint32_t slot) {
+        const uint64_t q = tile_desc(sbase + C::kQ + (PAIR ? s : qb) * qbytes, 16);
+        const uint64_t b = tile_desc(sbase + C::kKv + slot * C::kTileBytes, 16);
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x)
+          tc_mma_ss(col_s(s), q + (((x / 4) * qhalf + (x % 4) * 32) >> 4), b + (((x / 4) * C::kHalfBytes + (x % 4) * 32) >> 4),
+                    id_qk, x > 0);
+        tc_commit(s_full + s);
+        if (!PAIR || s == 1 || cnt1 == 0) tc_commit(empty + slot);
+      };
+      auto qk = [&](int s, int k) {  // from the stream's k-th tile
+        const uint32_t seq = 2 * kv + k_at(PAIR ? k : 2 * k + s), slot = seq % NS;
+        ok = ok && mbar_wait_warp(full + slot, (seq / NS) & 1, abort);
+        if (!ok) return;
         tc_fence_after();
-        // S of stream s from its k-th tile; the last reader of the K tile frees it
-        auto qk = [&](int s, int k) {
-          const long long seq = 2 * kv + k_at(PAIR ? k : 2 * k + s);
-          const int slot = (int)(seq % NS);
-          ok = ok && mbar_wait(full + slot, (uint32_t)((seq / NS) & 1), abort);
-          if (!ok) return;
-          tc_fence_after();
-          const uint64_t a = tile_desc(sbase + C::kQ + (PAIR ? s : qb) * qbytes, 16);
-          const uint64_t b = tile_desc(sbase + C::kKv + slot * C::kTileBytes, 16);
-#pragma unroll
-          for (int x = 0; x < D / 16; ++x) {
-            tc_mma_ss(col_s(s), a + (((x / 4) * qhalf + (x % 4) * 32) >> 4), b + (((x / 4) * C::kHalfBytes + (x % 4) * 32) >> 4),
-                      id_qk, x > 0);
-          }
-          tc_commit(s_full + s);
-          if (!PAIR || s == 1 || cnt1 == 0) tc_commit(empty + slot);
-        };
-        auto pv = [&](int s, int k) {
-          const long long seq = 2 * kv + v_at(g, PAIR ? k : 2 * k + s);
-          const int slot = (int)(seq % NS);
-          ok = ok && mbar_wait(p_ready + s, (ph_p >> s) & 1, abort);
-          ph_p ^= 1u << s;
-          ok = ok && mbar_wait(full + slot, (uint32_t)((seq / NS) & 1), abort);
-          if (!ok) return;
-          tc_fence_after();
-          const uint64_t b = tile_desc(sbase + C::kKv + slot * C::kTileBytes, C::kHalfBytes);
-#pragma unroll
-          for (int x = 0; x < kTile / 16; ++x) tc_mma_ts(col_o(s), col_s(s) + 8 * x, b + ((x * 2048) >> 4), id_pv, k > 0 || x > 0);
-          if (!PAIR || s == 1 || cnt1 == 0) tc_commit(empty + slot);
-          if (k == (s ? cnt1 : cnt0) - 1) tc_commit(o_full + s);
-        };
-        qk(0, 0);
-        if (cnt1 > 0) qk(1, 0);
-        for (int k = 0; ok && k < cnt0; ++k) {
-          pv(0, k);
-          if (k + 1 < cnt0) qk(0, k + 1);
-          if (k < cnt1) pv(1, k);
-          if (k + 1 < cnt1) qk(1, k + 1);
+        if (lead) mma_qk(s, slot);
+        __syncwarp();
+      };
+      // O of stream s from its k-th tile, then S of its next, with nothing in between where that K is in place
+      // (pair: waited for; split: the V slot may be what its load waits for)
+      auto step = [&](int s, int k) {
+        const bool more = k + 1 < (s ? cnt1 : cnt0);
+        const uint32_t vseq = 2 * kv + v_at(g, PAIR ? k : 2 * k + s), vslot = vseq % NS;
+        const uint32_t kseq = 2 * kv + k_at(PAIR ? k + 1 : 2 * k + 2 + s), kslot = kseq % NS;
+        const uint64_t v = tile_desc(sbase + C::kKv + vslot * C::kTileBytes, C::kHalfBytes);
+        ok = ok && mbar_wait_warp(full + vslot, (vseq / NS) & 1, abort);
+        bool next = false;
+        if (more && ok) {
+          if (PAIR)
+            next = ok = mbar_wait_warp(full + kslot, (kseq / NS) & 1, abort);
+          else
+            next = __all_sync(kFull, mbar_test_wait(full + kslot, (kseq / NS) & 1));
         }
-        if (ok) tc_commit(q_empty + qb);
-        kv += g.take;
+        ok = ok && mbar_wait_warp(p_ready + s, (ph_p >> s) & 1, abort);
+        ph_p ^= 1u << s;
+        if (!ok) return;
+        tc_fence_after();
+        if (lead) {
+#pragma unroll
+          for (int x = 0; x < kTile / 16; ++x) tc_mma_ts(col_o(s), col_s(s) + 8 * x, v + ((x * 2048) >> 4), id_pv, k > 0 || x > 0);
+          if (next) mma_qk(s, kslot);
+          if (!PAIR || s == 1 || cnt1 == 0) tc_commit(empty + vslot);
+          if (!more) tc_commit(o_full + s);
+        }
+        __syncwarp();
+        if (more && !next) qk(s, k + 1);
+      };
+      qk(0, 0);
+      if (cnt1 > 0) qk(1, 0);
+      for (int k = 0; ok && k < cnt0; ++k) {
+        step(0, k);
+        if (k < cnt1) step(1, k);
       }
-      if (!ok) {  // products in flight end before tensor memory is given back
-        *abort = 1;
+      if (ok && lead) tc_commit(q_empty + qb);
+      __syncwarp();
+      kv += g.take;
+    }
+    if (!ok) {  // products in flight end before tensor memory is given back
+      *abort = 1;
+      if (lead) {
         tc_commit(drain);
         const long long t0 = clock64();
         while (!mbar_try_wait(drain, 0) && clock64() - t0 < kWaitLimitCycles) {
         }
       }
+      __syncwarp();
     }
-    __syncwarp();
   } else if (warp == 9) {
     // ========================================================================= loads ====
     constexpr int N = E4M3 ? NR : NS;              // the ring that copies land in
@@ -857,7 +893,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
     const int pieces = kTile >> box_log2;
     const int piece = lane / kBoxes, col = lane % kBoxes;
     const bool mine = piece < pieces;  // (at most 16 pieces of 2 boxes)
-    long long seq = 0;
+    uint32_t seq = 0;  // (2^31 tiles a CTA are out of reach)
     SegIter<UR> it(plan);
     Seg g;
     while (ok && it.next(P, g)) {
@@ -871,8 +907,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
       };
       auto load = [&](bool v, int i, int page) {
         const int j = (g.nt - 1 - (g.off + i)) * kTile + (piece << box_log2);
-        const int slot = (int)(seq % N);
-        if (seq >= N) ok = mbar_wait_warp(eb + slot, (uint32_t)((seq / N - 1) & 1), abort);
+        const uint32_t slot = seq % N;
+        if (seq >= N) ok = mbar_wait_warp(eb + slot, (seq / N - 1) & 1, abort);
         if (!ok) return;
         if (lane == 0) mbar_arrive_expect(fb + slot, kStage);
         __syncwarp();
@@ -890,18 +926,17 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
         next = page_of(i + 2);
       }
     }
-    if (!ok) {  // copies in flight land before the CTA ends
-      *abort = 1;
-      const long long first = seq > N ? seq - N : 0;
-      for (long long x = first; x < seq; ++x) {
-        const long long t0 = clock64();
-        while (!mbar_try_wait(fb + x % N, (uint32_t)((x / N) & 1)) && clock64() - t0 < kWaitLimitCycles) {
-        }
+    if (!ok) *abort = 1;
+    // copies in flight land before the CTA ends, whoever gave up on them (else they have landed already)
+    for (uint32_t x = seq > N ? seq - N : 0; x < seq; ++x) {
+      const long long t0 = clock64();
+      while (!mbar_try_wait(fb + x % N, (x / N) & 1) && clock64() - t0 < kWaitLimitCycles) {
       }
     }
-  } else if (warp < 12) {
+  } else if (warp == 10) {
     // ======================================================================= queries ====
-    const int ql = tid - 320;  // 0..63
+    const int ql = lane;
+    int last = -1;  // the last segment whose queries were asked for
     SegIter<UR> it(plan);
     Seg g;
     for (int seg = 0; ok && it.next(P, g); ++seg) {
@@ -925,11 +960,12 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
             for (int y = 0; y < C::kHalves; ++y)
               tma_load_4d(qat + x * qbytes + y * qhalf, &P.qmap, y * 64, g.h * P.G, t0 + x * P.q_box, g.b, bar);
         }
+        last = seg;
         if (kConvert) ok = mbar_wait_warp(q_raw, (uint32_t)(seg & 1), abort);
         landing = bytes;
       } else {
         const unsigned char* q = P.q + ((long long)g.b * P.T * P.q_stride + (long long)g.h * P.G * D + ql % V * 8) * 2;
-        constexpr int R = 64 / V;  // rows a pass
+        constexpr int R = 32 / V;  // rows a pass
         int r = ql / V;
         int t = (int)fdiv((unsigned)(r0 + r), P.fd_g), gg = r0 + r - t * P.G;
         while (r < rows) {
@@ -951,16 +987,13 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
             }
           r += 8 * R;
         }
-        if (kConvert) {  // both warps' rows are in place
-          mbar_arrive(q_raw);
-          ok = mbar_wait_warp(q_raw, (uint32_t)(seg & 1), abort);
-        }
+        __syncwarp();
       }
       if constexpr (kConvert) {
         if (!ok) break;
         // bf16 to f16 in place: a power of two brings the row's largest finite magnitude to 2^14 .. 2^15, so
         // that only elements below 2^-38 of it lose bits
-        for (int r = ql; r < rows; r += 64) {
+        for (int r = ql; r < rows; r += 32) {
           const uint32_t at = qat + (r / kTile) * qbytes + (r % kTile) * 128;
           uint32_t top = 0;
 #pragma unroll 4
@@ -991,7 +1024,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
         }
         landing = 0;
       }
-      if (P.parents && warp == 10) {
+      if (P.parents) {
         Parent* pr = par + (PAIR ? 0 : qb * kTile);
         bool bad = false;
         for (int i = lane; i < g.n; i += 32) {
@@ -1007,11 +1040,19 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
       fence_proxy_async_shared();
       if (landing == 0 || ql > 0) mbar_arrive(q_full + qb);  // (thread 0 arrived with its copies)
     }
+    // these copies land, too
+    constexpr bool raw = E4M3 && !std::is_same<T, __half>::value;
+    for (int x = last; x >= 0 && x > last - (raw ? 1 : qbufs); --x) {
+      uint64_t* bar = raw ? q_raw : q_full + x % qbufs;
+      const long long t0 = clock64();
+      while (!mbar_try_wait(bar, (uint32_t)((raw ? x : x / qbufs) & 1)) && clock64() - t0 < kWaitLimitCycles) {
+      }
+    }
   } else {
     // ================================================================= codes to 16 bits ====
     if constexpr (E4M3) {
-      const int row = tid - 384;
-      long long seq = 0, kv = 0;
+      const int cw = warp - C::kConvert, row = (cw & 3) * 32 + lane, v = cw >= 4;  // four warps take the K tiles, four the V tiles
+      uint32_t kv = 0;
       SegIter<UR> it(plan);
       Seg g;
       while (ok && it.next(P, g)) {
@@ -1026,70 +1067,63 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
           const int j = (g.nt - 1 - (g.off + i)) * kTile + row;
           if (p < 0 || p >= P.num_pages) return make_float2(0.f, 0.f);
           const size_t at = (((size_t)p << P.page_log2) + (j & ((1 << P.page_log2) - 1))) * P.H + g.h;
-          return make_float2(__ldg(P.ks + at), __ldg(P.vs + at));
+          return make_float2(v ? 0.f : __ldg(P.ks + at), __ldg(P.vs + at));
         };
         // pages are fetched two tiles ahead, scales one
-        float2 was = make_float2(0.f, 0.f), now = scales_of(0, page_of(0)), next = scales_of(1, page_of(1));
-        int page = page_of(2), ve = 0, ve_next = 0;  // exponents of V(i - 1), V(i)
-        for (int i = 0; ok && i <= g.take; ++i) {  // K(i), V(i - 1)
-          for (int v = i < g.take ? 0 : 1; ok && v < (i > 0 ? 2 : 1); ++v) {
-            const int rs = (int)(seq % NR), slot = (int)(seq % NS);
-            if (seq >= NS) ok = mbar_wait_warp(empty + slot, (uint32_t)((seq / NS - 1) & 1), abort);
-            if (ok) ok = mbar_wait_warp(raw_full + rs, (uint32_t)((seq / NR) & 1), abort);
-            if (!ok) break;
-            // codes to f16, exactly
-            const uint32_t src = sbase + C::kRawAt + rs * C::kRawBytes + row * D;
-            const uint32_t dst = sbase + C::kKv + slot * C::kTileBytes + row * 128;
-            uint4 code[D / 16];
+        float2 now = scales_of(0, page_of(0));
+        int page = page_of(1);
+        for (int i = 0; ok && i < g.take; ++i) {
+          const float2 next = scales_of(i + 1, page);
+          page = page_of(i + 2);
+          const uint32_t seq = 2 * kv + (v ? v_at(g, i) : k_at(i)), rs = seq % NR, slot = seq % NS;
+          ok = mbar_wait_warp(raw_full + rs, (seq / NR) & 1, abort);
+          // (Place seq - NS may be the other warpgroup's.  It has its slot: the raw ring is no longer than this
+          // one, and a raw tile is given back only once its slot is had.  So at most one phase is to come.)
+          if (ok && seq >= NS) ok = mbar_wait_warp(empty + slot, (seq / NS - 1) & 1, abort);
+          if (!ok) break;
+          const uint32_t src = sbase + C::kRawAt + rs * C::kRawBytes + row * D;
+          const uint32_t dst = sbase + C::kKv + slot * C::kTileBytes + row * 128;
+          uint4 code[D / 16];
 #pragma unroll
-            for (int y = 0; y < D / 16; ++y) {
-              // the copy's swizzle: 16-byte pieces of a 128-byte row exchanged by its row of 8 (of a
-              // 64-byte row by its pair of rows of 4)
-              const int at = D == 128 ? (y ^ (row & 7)) : (y ^ ((row >> 1) & 3));
-              code[y] = lds128_at(src + (at << 4));
-            }
-            mbar_arrive(raw_empty + rs);  // (its codes are in registers)
-            // a scale goes with its codes in units of 2^e, e the exponent of the largest finite scale of this
-            // warp's 32 rows (V: within the range that the weights' reference exponent covers)
-            auto exponent = [](float x) {
-              const uint32_t mag = __float_as_uint(fabsf(x));
-              return (int)(__reduce_max_sync(kFull, mag < 0x7f800000u ? mag : 0u) >> 23) - 127;
-            };
-            int e = ve;
-            if (!v) {
-              e = max(-126, exponent(now.x));
-              ve_next = max(-60, min(100, exponent(now.y)));
-              if (lane == 0) {
-                int* at = exps + (int)((kv + i) % ES) * 8 + (warp & 3);
-                at[0] = e;
-                at[4] = ve_next;
-              }
-            }
-            const __half2 rel = __float2half2_rn((v ? was.y : now.x) * __uint_as_float((uint32_t)(127 - e) << 23));
-#pragma unroll
-            for (int y = 0; y < D / 16; ++y) {
-              const uint32_t w[4] = {code[y].x, code[y].y, code[y].z, code[y].w};
-              uint32_t o[8];
-#pragma unroll
-              for (int z = 0; z < 8; ++z) {
-                uint32_t h;
-                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(w[z >> 1] >> (16 * (z & 1)))));
-                const __half2 f = __hmul2(*reinterpret_cast<const __half2*>(&h), rel);
-                o[z] = *reinterpret_cast<const uint32_t*>(&f);
-              }
-              const int h = y / 4, c = 2 * (y % 4);
-              sts128(dst + h * C::kHalfBytes + ((c ^ (row & 7)) << 4), o[0], o[1], o[2], o[3]);
-              sts128(dst + h * C::kHalfBytes + (((c + 1) ^ (row & 7)) << 4), o[4], o[5], o[6], o[7]);
-            }
-            fence_proxy_async_shared();
-            mbar_arrive(full + slot);
-            ++seq;
+          for (int y = 0; y < D / 16; ++y) {
+            // the copy's swizzle: 16-byte pieces of a 128-byte row exchanged by its row of 8 (of a
+            // 64-byte row by its pair of rows of 4)
+            const int at = D == 128 ? (y ^ (row & 7)) : (y ^ ((row >> 1) & 3));
+            code[y] = lds128_at(src + (at << 4));
           }
-          was = now;
-          ve = ve_next;
+          mbar_arrive_warp(raw_empty + rs);  // (its codes are in registers)
+          // a scale goes with its codes in units of 2^e, e the exponent of the largest finite scale of this
+          // warp's 32 rows (V: within the range that the weights' reference exponent covers)
+          auto exponent = [](float x) {
+            const uint32_t mag = __float_as_uint(fabsf(x));
+            return (int)(__reduce_max_sync(kFull, mag < 0x7f800000u ? mag : 0u) >> 23) - 127;
+          };
+          const int ve = max(-60, min(100, exponent(now.y)));
+          const int e = v ? ve : max(-126, exponent(now.x));
+          if (!v && lane == 0) {
+            int* at = exps + (kv + i) % ES * 8 + cw;
+            at[0] = e;
+            at[4] = ve;
+          }
+          const __half2 rel = __float2half2_rn((v ? now.y : now.x) * __uint_as_float((uint32_t)(127 - e) << 23));
+#pragma unroll
+          for (int y = 0; y < D / 16; ++y) {
+            const uint32_t w[4] = {code[y].x, code[y].y, code[y].z, code[y].w};
+            uint32_t o[8];
+#pragma unroll
+            for (int z = 0; z < 8; ++z) {
+              uint32_t h;
+              asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(w[z >> 1] >> (16 * (z & 1)))));
+              const __half2 f = __hmul2(*reinterpret_cast<const __half2*>(&h), rel);
+              o[z] = *reinterpret_cast<const uint32_t*>(&f);
+            }
+            const int h = y / 4, c = 2 * (y % 4);
+            sts128(dst + h * C::kHalfBytes + ((c ^ (row & 7)) << 4), o[0], o[1], o[2], o[3]);
+            sts128(dst + h * C::kHalfBytes + (((c + 1) ^ (row & 7)) << 4), o[4], o[5], o[6], o[7]);
+          }
+          fence_proxy_async_shared();
+          mbar_arrive_warp(full + slot);
           now = next;
-          next = scales_of(i + 2, page);
-          page = page_of(i + 3);
         }
         kv += g.take;
       }
