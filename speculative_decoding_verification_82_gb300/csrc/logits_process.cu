@@ -4,17 +4,19 @@
 // Row n's rules depend on the request (history counts, biases), the row (its mask) and the path from
 // the root to n (the draft tokens accepted if n is).  One block takes a chunk of the vocabulary of
 // one request and a group of its rows:
-//   1. it scans the request's history and biases once and keeps what falls into its chunk in shared
-//      memory: a 32-bit entry per token (occurrences in the output; whether it is in the prompt;
-//      whether it has a bias) and a bitmap of the tokens with an entry;
+//   1. it scans the request's history, biases and drafted tokens once and keeps what falls into its chunk in
+//      shared memory: a 32-bit entry per token (occurrences in the output; whether it is in the prompt;
+//      whether it has a bias) and a list of the tokens that have an entry or are drafted;
 //   2. it links every node to the nearest ancestor whose token lies in the chunk, so that a row's
-//      path tokens in the chunk are a short list (most often empty);
-//   3. it streams the rows' 16-byte vectors.  A vector whose bits in the bitmap and in the row's
-//      mask are all trivial, as nearly all are, passes through untouched; only tokens with a bit
-//      set look up their entry.
-// The bitmaps are read at any bit offset, so rows whose start is not 16-byte aligned (an odd
-// vocabulary) take the same path.  Each logit is read and written once: the kernel is bound by HBM
-// bandwidth.  In place (out == logits), a vector that no rule touches is neither read nor written.
+//      path tokens in the chunk are a short chain (most often empty);
+//   3. it streams the rows' 16-byte vectors from input to output, with -inf where the mask has a zero;
+//   4. it goes over the listed tokens of every row, spread evenly over its threads, and applies their rules
+//      to the input's logits (a few hundred elements of a block's 65,536, most of them in the chunks of the
+//      frequent, small ids: handled where their vectors stream, they held up whole warps and blocks:
+//      134 -> 92 us on 16 61-node trees of 128,256 bf16 logits).
+// Mask bits are read at any offset, so rows whose start is not 16-byte aligned (an odd vocabulary) take the
+// same steps, with partial vectors at their ends.  Each logit is read and written once: the kernel is bound by
+// HBM bandwidth.  In place (out == logits), a vector that no rule touches is neither read nor written.
 //
 // The arithmetic is in 32 bits with one rounding per step of the definition (no contraction), and
 // sums of integer counts and of biases in list order, so results do not depend on the launch.
@@ -25,6 +27,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include "fastdiv.h"
 #include "spec_verify.h"
 
 namespace {
@@ -32,7 +35,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxRows = SPEC_MAX_LOGITS_ROWS;
 constexpr int kMaxChunk = 4096;  // tokens per block
-constexpr int kUnroll = 4;       // vectors a thread has in flight
+constexpr int kRowsAtOnce = 4;   // rows whose vectors a thread has in flight together
+constexpr int kMaxGroup = 8;     // rows per block (16 and 61 rows: 115 and 121 us where 8 take 108)
+constexpr int kScan = 8;         // history tokens a thread has in flight
 constexpr uint32_t kPromptBit = 0x80000000u, kBiasBit = 0x40000000u, kCountMask = 0x3fffffffu;
 constexpr uint16_t kOutside = 0xffff;
 
@@ -40,7 +45,8 @@ struct LogitsParams {
   const unsigned char* in;
   unsigned char* out;
   int B, R, V, W, Lmax, nb;
-  int chunk, rows_per_block;
+  int chunk, rows_per_block, groups;
+  specv::FastDiv fd_b, fd_groups;
   const int32_t *history, *history_len, *prompt_len;
   const int32_t *draft_tokens, *node_tokens, *parents;
   const float *repetition, *presence, *frequency;
@@ -58,7 +64,6 @@ struct Fmt<float> {
   using Raw = uint32_t;
   __device__ static float get(uint32_t w, int) { return __uint_as_float(w); }
   __device__ static Raw raw(float f) { return __float_as_uint(f); }
-  __device__ static uint32_t put(uint32_t, int, float f) { return __float_as_uint(f); }
 };
 template <>
 struct Fmt<__nv_bfloat16> {
@@ -66,10 +71,6 @@ struct Fmt<__nv_bfloat16> {
   using Raw = uint16_t;
   __device__ static float get(uint32_t w, int hi) { return __uint_as_float(hi ? (w & 0xffff0000u) : (w << 16)); }
   __device__ static Raw raw(float f) { return __bfloat16_as_ushort(__float2bfloat16_rn(f)); }
-  __device__ static uint32_t put(uint32_t w, int hi, float f) {
-    const uint32_t r = raw(f);
-    return hi ? ((w & 0xffffu) | (r << 16)) : ((w & 0xffff0000u) | r);
-  }
 };
 template <>
 struct Fmt<__half> {
@@ -79,10 +80,6 @@ struct Fmt<__half> {
     return __half2float(__ushort_as_half((unsigned short)(hi ? (w >> 16) : (w & 0xffffu))));
   }
   __device__ static Raw raw(float f) { return __half_as_ushort(__float2half_rn(f)); }
-  __device__ static uint32_t put(uint32_t w, int hi, float f) {
-    const uint32_t r = raw(f);
-    return hi ? ((w & 0xffffu) | (r << 16)) : ((w & 0xffff0000u) | r);
-  }
 };
 
 // One request's penalties.
@@ -97,24 +94,31 @@ __device__ __forceinline__ float apply_rules(float x, uint32_t entry, uint32_t p
   return x;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) logits_process_kernel(const LogitsParams P) {
+// ALIGNED: every row starts on a 16-byte boundary, in both buffers.
+template <typename T, bool ALIGNED>
+__global__ void __launch_bounds__(kThreads, sizeof(typename Fmt<T>::Raw) == 4 ? 4 : 6) logits_process_kernel(const LogitsParams P) {
   constexpr int VE = Fmt<T>::VE, S = 16 / VE;
   using Raw = typename Fmt<T>::Raw;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ uint16_t par[kMaxRows], ltok[kMaxRows], up[kMaxRows];
   __shared__ uint32_t bitmap[kMaxChunk / 32 + 3];
+  __shared__ int listed;
   const int span = P.chunk + VE;  // tokens with an entry: a chunk's last vector may reach past its end
   uint32_t* table = reinterpret_cast<uint32_t*>(smem);
-  float* bias_sum = reinterpret_cast<float*>(smem) + span;  // only with biases
-  const int b = blockIdx.y, t = threadIdx.x;
-  const int t0 = blockIdx.x * P.chunk;
+  uint16_t* list = reinterpret_cast<uint16_t*>(table + span);  // tokens with an entry or drafted, in any order
+  float* bias_sum = reinterpret_cast<float*>(list + span);      // only with biases (span is even)
+  // blocks run chunk by chunk: the first chunks, which have most rules, are not left to the end
+  const unsigned cg = specv::fdiv(blockIdx.x, P.fd_b);
+  const int b = (int)(blockIdx.x - cg * P.fd_b.d), t = threadIdx.x;
+  const int chunk = (int)specv::fdiv(cg, P.fd_groups), group = (int)cg - chunk * P.groups;
+  const int t0 = chunk * P.chunk;
   const int t_end = min(P.V, t0 + span);
   const int words = span / 32 + 2;
 
   // -- 1. the request's lengths, penalties and tree
   for (int i = t; i < span; i += kThreads) table[i] = 0;
   for (int i = t; i < words; i += kThreads) bitmap[i] = 0;
+  if (t == 0) listed = 0;
   int len = 0, plen = 0, flags = 0;
   if (P.history) {
     len = __ldg(P.history_len + b);
@@ -143,21 +147,30 @@ __global__ void __launch_bounds__(kThreads) logits_process_kernel(const LogitsPa
   }
   if (__syncthreads_or(bad_tree)) flags |= SPEC_ERRF_BAD_TREE;
   if (__syncthreads_or(bad_token)) flags |= SPEC_ERRF_BAD_TOKEN;
-  if (P.err_flags && blockIdx.x == 0 && blockIdx.z == 0 && t == 0) P.err_flags[b] = flags;
+  if (P.err_flags && chunk == 0 && group == 0 && t == 0) P.err_flags[b] = flags;
   const bool plain = flags != 0;  // the rows come out unprocessed
 
   // -- 2. the chunk's entries
   if (!plain) {
     const int32_t* h = P.history + (size_t)b * P.Lmax;
-    for (int j = t; j < len; j += kThreads) {
-      const int tok = __ldg(h + j);
-      if (tok < t0 || tok >= t_end) continue;
-      const int l = tok - t0;
-      if (j < plen)
-        atomicOr(&table[l], kPromptBit);
-      else
-        atomicAdd(&table[l], 1u);
-      atomicOr(&bitmap[l >> 5], 1u << (l & 31));
+    for (int j0 = t; j0 < len; j0 += kThreads * kScan) {
+      int tok[kScan];
+#pragma unroll
+      for (int u = 0; u < kScan; ++u) {
+        const int j = j0 + u * kThreads;
+        tok[u] = j < len ? __ldg(h + j) : -1;
+      }
+#pragma unroll
+      for (int u = 0; u < kScan; ++u) {
+        const int j = j0 + u * kThreads;
+        if (tok[u] < t0 || tok[u] >= t_end) continue;
+        const int l = tok[u] - t0;
+        if (j < plen)
+          atomicOr(&table[l], kPromptBit);
+        else
+          atomicAdd(&table[l], 1u);
+        atomicOr(&bitmap[l >> 5], 1u << (l & 31));
+      }
     }
     const int32_t* bt = P.bias_tokens + (size_t)b * P.nb;
     const float* bv = P.bias_values + (size_t)b * P.nb;
@@ -181,103 +194,144 @@ __global__ void __launch_bounds__(kThreads) logits_process_kernel(const LogitsPa
       int m = path ? n : 0;
       while (m > 0 && ltok[m] == kOutside) m = par[m];
       up[n] = (uint16_t)m;
+      if (path && ltok[n] != kOutside) atomicOr(&bitmap[ltok[n] >> 5], 1u << (ltok[n] & 31));
+    }
+    __syncthreads();
+    for (int i = t; i < words; i += kThreads) {
+      uint32_t bits = bitmap[i];
+      if (!bits) continue;
+      for (int at = atomicAdd(&listed, __popc(bits)); bits; bits &= bits - 1) list[at++] = (uint16_t)(32 * i + __ffs(bits) - 1);
     }
   }
   __syncthreads();
 
-  // -- 3. the rows
+  // -- 3. the rows' vectors
   const bool in_place = P.in == P.out;
-  const int r0 = blockIdx.z * P.rows_per_block, r1 = min(P.R, r0 + P.rows_per_block);
-  for (int r = r0; r < r1; ++r) {
-    const size_t row = ((size_t)b * P.R + r) * (size_t)P.V;
-    const unsigned char* in = P.in + row * S;
-    unsigned char* out = P.out + row * S;
-    const int a = (int)(((uintptr_t)in & 15u) / S);  // elements before the row in its first vector
-    const bool same = (((uintptr_t)in ^ (uintptr_t)out) & 15u) == 0;
-    const uint32_t* mask = P.allowed ? P.allowed + ((size_t)b * P.R + r) * (size_t)P.W : nullptr;
-    const int head = plain ? 0 : up[r];
-    // this block's vectors: those whose first token (v VE - a) lies in [t0, t0 + chunk); block 0 also
-    // takes the one that starts before the row
-    const int v0 = t0 == 0 ? 0 : (t0 + a + VE - 1) / VE;
-    const int v1 = (min(P.V, t0 + P.chunk) + a + VE - 1) / VE;
-    for (int vb = v0; vb < v1; vb += kThreads * kUnroll) {
-      uint4 x[kUnroll];
-      uint32_t nz[kUnroll], ban[kUnroll];  // bits: tokens with an entry or on the path; not allowed
+  constexpr uint32_t kAll = (1u << VE) - 1u;
+  constexpr int per = VE / 4;  // elements of a word
+  const int r0 = group * P.rows_per_block, r1 = min(P.R, r0 + P.rows_per_block);
+  const int stop = min(P.V, t0 + P.chunk);
+  const uint32_t inf = (uint32_t)Fmt<T>::raw(-INFINITY);
+
+  auto forbid = [&](uint4& x, uint32_t ban) {  // -inf where ban has a bit
+    uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int v = vb + u * kThreads + t;
-        nz[u] = ban[u] = 0;
-        if (v >= v1) continue;
-        const int tok = v * VE - a;
-        const bool whole = tok >= 0 && tok + VE <= P.V;
-        if (!plain) {
-          // bit i is token tok + i; tok may be negative in block 0's first vector only
-          const int l = tok - t0;
-          const int ls = l < 0 ? 0 : l;
-          nz[u] = __funnelshift_r(bitmap[ls >> 5], bitmap[(ls >> 5) + 1], ls & 31);
-          if (l < 0) nz[u] <<= -l;
-          for (int m = head; m > 0; m = up[par[m]]) {
-            const int d = (int)ltok[m] - l;
-            if (d >= 0 && d < VE) nz[u] |= 1u << d;
-          }
-          if (mask) {
-            const int ts = tok < 0 ? 0 : tok, w = ts >> 5;
-            const uint32_t lo = ~__ldg(mask + w), hi = w + 1 < P.W ? ~__ldg(mask + w + 1) : 0u;
-            ban[u] = __funnelshift_r(lo, hi, ts & 31);
-            if (tok < 0) ban[u] <<= -tok;
-          }
-          const uint32_t all = (1u << VE) - 1u;
-          nz[u] &= all;
-          ban[u] &= all;
-        }
-        if (whole && (!in_place || (nz[u] | ban[u]))) x[u] = __ldcs(reinterpret_cast<const uint4*>(in + (long long)tok * S));
+    for (int y = 0; y < 4; ++y) {
+      if (per == 1) {
+        w[y] = ban >> y & 1u ? inf : w[y];
+      } else {
+        const uint32_t two = ban >> (2 * y);
+        w[y] = two & 1u ? (w[y] & 0xffff0000u) | inf : w[y];
+        w[y] = two & 2u ? (w[y] & 0xffffu) | (inf << 16) : w[y];
       }
+    }
+    x = make_uint4(w[0], w[1], w[2], w[3]);
+  };
+
+  if constexpr (ALIGNED) {
+    // kRowsAtOnce rows at a time: their vectors are in flight together
+    for (int ra = r0; ra < r1; ra += kRowsAtOnce) {
+      const size_t row = ((size_t)b * P.R + ra) * (size_t)P.V;
+      const unsigned char* in = P.in + row * S;
+      unsigned char* out = P.out + row * S;
+      const uint32_t* mask = P.allowed && !plain ? P.allowed + ((size_t)b * P.R + ra) * (size_t)P.W : nullptr;
+      if (in_place && !mask) break;
+      const size_t pitch = (size_t)P.V * S;
+      bool has[kRowsAtOnce];
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int v = vb + u * kThreads + t;
-        if (v >= v1) continue;
-        const int tok = v * VE - a;
-        const bool whole = tok >= 0 && tok + VE <= P.V;
-        const uint32_t touched = nz[u] | ban[u];
-        if (in_place && !touched) continue;
-        const int l = tok - t0;
-        auto value = [&](float f, int i) {  // token tok + i with value f, under its rules
-          if (ban[u] >> i & 1u) return -INFINITY;
-          uint32_t n = 0;
-          for (int m = head; m > 0; m = up[par[m]]) n += (int)ltok[m] == l + i;
-          const uint32_t entry = table[l + i];
-          return apply_rules(f, entry, n, q, (entry & kBiasBit) ? bias_sum[l + i] : 0.f);
-        };
-        if (whole) {
-          uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-          if (touched) {
+      for (int u = 0; u < kRowsAtOnce; ++u) has[u] = ra + u < r1;
+      for (int tk = t0 + t * VE; tk < stop; tk += kThreads * VE) {
+        uint4 x[kRowsAtOnce];
+        uint32_t ban[kRowsAtOnce];
 #pragma unroll
-            for (int i = 0; i < VE; ++i)
-              if (touched >> i & 1u) {
-                constexpr int per = VE / 4;
-                w[i / per] = Fmt<T>::put(w[i / per], i % per, value(Fmt<T>::get(w[i / per], i % per), i));
-              }
+        for (int u = 0; u < kRowsAtOnce; ++u)
+          ban[u] = mask && has[u] ? ~__ldg(mask + (size_t)u * P.W + (tk >> 5)) >> (tk & 31) & kAll : 0u;
+#pragma unroll
+        for (int u = 0; u < kRowsAtOnce; ++u)
+          if (has[u] && (!in_place || ban[u])) x[u] = *reinterpret_cast<const uint4*>(in + u * pitch + (size_t)tk * S);
+#pragma unroll
+        for (int u = 0; u < kRowsAtOnce; ++u) {
+          if (ban[u]) forbid(x[u], ban[u]);
+          if (has[u] && (!in_place || ban[u])) *reinterpret_cast<uint4*>(out + u * pitch + (size_t)tk * S) = x[u];
+        }
+      }
+    }
+  } else {
+    // likewise, a row's vectors starting `a` elements before it: this block's are those whose first token lies
+    // in [t0, stop), in block 0 also the one that starts before the row
+    for (int ra = r0; ra < r1; ra += kRowsAtOnce) {
+      const size_t row = ((size_t)b * P.R + ra) * (size_t)P.V;
+      const uint32_t* mask = P.allowed && !plain ? P.allowed + ((size_t)b * P.R + ra) * (size_t)P.W : nullptr;
+      if (in_place && !mask) break;
+      const size_t pitch = (size_t)P.V * S;
+      for (int v = t0 / VE + t; v <= (stop + VE - 1) / VE; v += kThreads) {
+        uint4 x[kRowsAtOnce];
+        uint32_t ban[kRowsAtOnce];
+        int tk[kRowsAtOnce];  // the vector's first token; P.V: not this block's
+#pragma unroll
+        for (int u = 0; u < kRowsAtOnce; ++u) {
+          const unsigned char* in = P.in + row * S + u * pitch;
+          tk[u] = v * VE - (int)(((uintptr_t)in & 15u) / S);
+          ban[u] = 0;
+          if (ra + u >= r1 || tk[u] >= stop || (tk[u] < t0 && t0 > 0)) tk[u] = P.V;
+          if (tk[u] >= P.V) continue;
+          if (mask) {  // bit i is token tk + i
+            const uint32_t* m = mask + (size_t)u * P.W;
+            const int ts = max(tk[u], 0), w = ts >> 5;
+            ban[u] = __funnelshift_r(~__ldg(m + w), w + 1 < P.W ? ~__ldg(m + w + 1) : 0u, ts & 31);
+            if (tk[u] < 0) ban[u] <<= -tk[u];
+            ban[u] &= kAll;
           }
-          if (same) {
-            *reinterpret_cast<uint4*>(out + (long long)tok * S) = make_uint4(w[0], w[1], w[2], w[3]);
-          } else {
+          if (tk[u] >= 0 && tk[u] + VE <= P.V && (!in_place || ban[u]))
+            x[u] = *reinterpret_cast<const uint4*>(in + (size_t)tk[u] * S);
+        }
 #pragma unroll
-            for (int i = 0; i < VE; ++i) {
-              const uint32_t word = w[i / (VE / 4)];
-              *reinterpret_cast<Raw*>(out + (long long)(tok + i) * S) =
-                  (Raw)(VE == 8 && (i & 1) ? word >> 16 : word);
+        for (int u = 0; u < kRowsAtOnce; ++u) {
+          if (tk[u] >= P.V || (in_place && !ban[u])) continue;
+          const unsigned char* in = P.in + row * S + u * pitch + (long long)tk[u] * S;
+          unsigned char* out = P.out + row * S + u * pitch + (long long)tk[u] * S;
+          if (tk[u] >= 0 && tk[u] + VE <= P.V) {
+            if (ban[u]) forbid(x[u], ban[u]);
+            if ((((uintptr_t)in ^ (uintptr_t)out) & 15u) == 0) {
+              *reinterpret_cast<uint4*>(out) = x[u];
+            } else {
+              const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+              for (int i = 0; i < VE; ++i)
+                *reinterpret_cast<Raw*>(out + i * S) = (Raw)(per == 2 && (i & 1) ? w[i / per] >> 16 : w[i / per]);
             }
-          }
-        } else {  // the row's ends, element by element
-          for (int i = 0; i < VE; ++i) {
-            if (tok + i < 0 || tok + i >= P.V) continue;
-            Raw e = *reinterpret_cast<const Raw*>(in + (long long)(tok + i) * S);
-            if (touched >> i & 1u) e = Fmt<T>::raw(value(Fmt<T>::get(e, 0), i));
-            *reinterpret_cast<Raw*>(out + (long long)(tok + i) * S) = e;
+          } else {  // the row's ends, element by element
+            for (int i = 0; i < VE; ++i)
+              if (tk[u] + i >= 0 && tk[u] + i < P.V)
+                *reinterpret_cast<Raw*>(out + i * S) = ban[u] >> i & 1u ? (Raw)inf : *reinterpret_cast<const Raw*>(in + i * S);
           }
         }
       }
     }
+  }
+  if (plain || listed == 0) return;
+  __syncthreads();  // the rules' elements are written over the vectors'
+
+  // -- 4. the listed tokens, row by row, spread over the threads
+  const int n = listed;
+  int r = r0, k = t;
+  for (;;) {
+    while (k >= n && r < r1) k -= n, ++r;
+    if (r >= r1) break;
+    const int l = list[k], tok = t0 + l;
+    k += kThreads;
+    const size_t row = ((size_t)b * P.R + r) * (size_t)P.V;
+    if (!ALIGNED) {  // whose is the vector it lies in?
+      const int a = (int)(((uintptr_t)(P.in + row * S) & 15u) / S), first = (tok + a) / VE * VE - a;
+      if ((first < t0 && t0 > 0) || first >= stop) continue;
+    }
+    uint32_t c = 0;
+    for (int m = up[r]; m > 0; m = up[par[m]]) c += ltok[m] == l;
+    const uint32_t entry = table[l];
+    if (!entry && !c) continue;  // drafted, but not on this row's path
+    if (P.allowed && !(__ldg(P.allowed + ((size_t)b * P.R + r) * (size_t)P.W + (tok >> 5)) >> (tok & 31) & 1u)) continue;
+    const float f = Fmt<T>::get(*reinterpret_cast<const Raw*>(P.in + (row + tok) * S), 0);
+    *reinterpret_cast<Raw*>(P.out + (row + tok) * S) = Fmt<T>::raw(apply_rules(f, entry, c, q, (entry & kBiasBit) ? bias_sum[l] : 0.f));
   }
 }
 
@@ -293,8 +347,12 @@ int sm_count_cached() {
 }
 
 template <typename T>
-spec_status_t launch(const LogitsParams& P, dim3 grid, size_t smem, cudaStream_t stream) {
-  logits_process_kernel<T><<<grid, kThreads, smem, stream>>>(P);
+spec_status_t launch(const LogitsParams& P, unsigned grid, size_t smem, cudaStream_t stream) {
+  const bool aligned = (((uintptr_t)P.in | (uintptr_t)P.out | ((uintptr_t)P.V * (16 / Fmt<T>::VE))) & 15u) == 0;
+  if (aligned)
+    logits_process_kernel<T, true><<<grid, kThreads, smem, stream>>>(P);
+  else
+    logits_process_kernel<T, false><<<grid, kThreads, smem, stream>>>(P);
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
@@ -351,11 +409,15 @@ extern "C" spec_status_t spec_logits_process(const void* logits, spec_dtype_t dt
   auto chunks = [&] { return ((long long)V + P.chunk - 1) / P.chunk; };
   while (P.chunk > 1024 && chunks() * B < want) P.chunk /= 2;
   long long groups = (want + chunks() * B - 1) / (chunks() * B);
+  if (groups < (R + kMaxGroup - 1) / kMaxGroup) groups = (R + kMaxGroup - 1) / kMaxGroup;
   if (groups > R) groups = R;
-  if (groups < 1) groups = 1;
   P.rows_per_block = (int)((R + groups - 1) / groups);
-  const dim3 grid((unsigned)chunks(), (unsigned)B, (unsigned)((R + P.rows_per_block - 1) / P.rows_per_block));
-  const size_t smem = (size_t)(P.chunk + 8) * 4 * (num_biases > 0 ? 2 : 1);  // at most 32,832 bytes beside 6.7 KB static
+  P.groups = (int)((R + P.rows_per_block - 1) / P.rows_per_block);
+  if (chunks() * P.groups > INT_MAX / B) return SPEC_ERR_UNSUPPORTED;
+  P.fd_b = specv::make_fastdiv((uint32_t)B);
+  P.fd_groups = specv::make_fastdiv((uint32_t)P.groups);
+  const unsigned grid = (unsigned)(chunks() * P.groups * B);
+  const size_t smem = (size_t)(P.chunk + 8) * (num_biases > 0 ? 10 : 6);  // at most 41,040 bytes beside 6.7 KB static
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (dtype == SPEC_DTYPE_F32) return launch<float>(P, grid, smem, st);
   if (dtype == SPEC_DTYPE_BF16) return launch<__nv_bfloat16>(P, grid, smem, st);
