@@ -100,6 +100,9 @@ def _stream(device) -> c_void_p:
 
 
 def _need(t, name: str, dtype, shape, device) -> torch.Tensor:
+    if (isinstance(t, torch.Tensor) and t.device == device and (dtype is None or t.dtype == dtype)
+            and t.shape == shape and t.is_contiguous()):
+        return t
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.device != device:
@@ -326,12 +329,16 @@ def spec_kv_compact(caches, slots, parents, accept_len, path_nodes, *, err_flags
 
 
 def _call(fn, device, *args) -> None:
-    """fn(*args, the current stream of `device`) with `device` current, its status checked."""
+    """fn(*args, the current stream of `device`) with `device` current, its status checked.  Tensors among
+    the arguments become their addresses."""
+    args = [a.data_ptr() if isinstance(a, torch.Tensor) else a for a in args]
     if device.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(device)))
+        status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
     else:
         with torch.cuda.device(device):
-            _check(fn(*args, _stream(device)))
+            status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    if status != SPEC_OK:
+        _check(status)
 
 
 def _cuda(t, name: str):
@@ -391,10 +398,10 @@ def spec_logits_process(logits, *, history=None, history_len=None, prompt_len=No
     a, z, n = logits.data_ptr(), o.data_ptr(), logits.numel() * logits.element_size()
     if a != z and a < z + n and z < a + n:
         raise ValueError("out logits must be logits itself or not overlap it")
-    _call(lib.spec_logits_process, dev, _ptr(logits), DTYPE_CODE[logits.dtype], B, R, V, _ptr(history),
-          _ptr(history_len), _ptr(prompt_len), Lmax, _ptr(draft_tokens), _ptr(node_tokens), _ptr(parents),
-          _ptr(repetition), _ptr(presence), _ptr(frequency), _ptr(bias_tokens), _ptr(bias_values), nb,
-          _ptr(allowed), _ptr(o), _ptr(ef))
+    _call(lib.spec_logits_process, dev, logits, DTYPE_CODE[logits.dtype], B, R, V, history,
+          history_len, prompt_len, Lmax, draft_tokens, node_tokens, parents,
+          repetition, presence, frequency, bias_tokens, bias_values, nb,
+          allowed, o, ef)
     return dict(logits=o, err_flags=ef)
 
 
@@ -446,8 +453,8 @@ def spec_kv_write(k, v, k_cache, v_cache, slots, *, k_scale=None, v_scale=None, 
         raise ValueError(f"the caches hold {Hc} heads of {Dc}, k and v {H} of {D}")
     _need(slots, "slots", torch.int32, (B, T), dev)
     ef = _out(err_flags, "err_flags", torch.int32, (B,), dev)
-    _call(lib.spec_kv_write, dev, _ptr(k), _ptr(v), DTYPE_CODE[k.dtype], ks, vs, B, T, H, D, _ptr(slots),
-          _ptr(k_cache), _ptr(v_cache), CACHE_CODE[k_cache.dtype], _ptr(k_scale), _ptr(v_scale), S, _ptr(ef))
+    _call(lib.spec_kv_write, dev, k, v, DTYPE_CODE[k.dtype], ks, vs, B, T, H, D, slots,
+          k_cache, v_cache, CACHE_CODE[k_cache.dtype], k_scale, v_scale, S, ef)
     return ef
 
 
@@ -466,8 +473,8 @@ def spec_kv_read(k_cache, v_cache, slots, dtype, *, k_scale=None, v_scale=None, 
     ko = _out(out.get("k"), "out k", dtype, (B, T, H, D), dev)
     vo = _out(out.get("v"), "out v", dtype, (B, T, H, D), dev)
     ef = _out(out.get("err_flags"), "err_flags", torch.int32, (B,), dev)
-    _call(lib.spec_kv_read, dev, _ptr(k_cache), _ptr(v_cache), CACHE_CODE[k_cache.dtype], _ptr(k_scale), _ptr(v_scale),
-          S, B, T, H, D, _ptr(slots), _ptr(ko), _ptr(vo), DTYPE_CODE[dtype], _ptr(ef))
+    _call(lib.spec_kv_read, dev, k_cache, v_cache, CACHE_CODE[k_cache.dtype], k_scale, v_scale,
+          S, B, T, H, D, slots, ko, vo, DTYPE_CODE[dtype], ef)
     return dict(k=ko, v=vo, err_flags=ef)
 
 
@@ -514,8 +521,8 @@ def spec_attention(q, k_cache, v_cache, page_table, context_len, *, chunk_len=No
     out = out or {}
     o = _out(out.get("out"), "out", q.dtype, (B, T, Hq, D), dev)
     ef = _out(out.get("err_flags"), "err_flags", torch.int32, (B,), dev)
-    _call(lib.spec_attention, dev, _ptr(q), DTYPE_CODE[q.dtype], qs, B, T, Hq, H, D, _ptr(k_cache), _ptr(v_cache),
-          CACHE_CODE[k_cache.dtype], _ptr(k_scale), _ptr(v_scale), k_cache.shape[0], k_cache.shape[1], _ptr(page_table),
-          P, _ptr(context_len), _ptr(chunk_len), _ptr(parents), D**-0.5 if scale is None else float(scale), _ptr(o),
-          _ptr(lse), _ptr(ef), _ptr(workspace), workspace.numel() * workspace.element_size())
+    _call(lib.spec_attention, dev, q, DTYPE_CODE[q.dtype], qs, B, T, Hq, H, D, k_cache, v_cache,
+          CACHE_CODE[k_cache.dtype], k_scale, v_scale, k_cache.shape[0], k_cache.shape[1], page_table,
+          P, context_len, chunk_len, parents, D**-0.5 if scale is None else float(scale), o,
+          lse, ef, workspace, workspace.numel() * workspace.element_size())
     return dict(out=o, lse=lse, err_flags=ef)

@@ -9,9 +9,11 @@
 // against a / 448 and no precision above the subnormal codes.
 //
 // Both kernels stream every byte once and are bound by HBM bandwidth, or by launch latency for a
-// draft tree's few rows.  A row belongs to the smallest power of two of lanes that covers it with 8
-// elements each (16 lanes for 128), so its maximum is a few shuffles and every lane moves one
-// 16-byte vector of 16-bit input.
+// draft tree's few rows.  A row belongs to the smallest power of two of lanes that covers it with 16 (8 where
+// head_dim asks for it) elements each, 8 lanes for 128, so its maximum is a few shuffles and every lane moves
+// whole 16-byte vectors of codes; a thread has two rows in flight.  (One row and 8 elements a thread:
+// 46 us where this takes KVREAD on 16 x 2052 tokens of 8 heads of 128 read to bf16, 15.5 where this takes KVWRITE
+// on 4 x 2048 f16 tokens written.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <limits.h>
@@ -23,7 +25,7 @@
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kElems = 8;  // elements of a row per lane
+constexpr int kRowsPerThread = 2;
 
 struct KvRows {
   const unsigned char* src[2];  // write: k, v rows; read: the caches
@@ -120,6 +122,13 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t two) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+// The u-th row of this thread: a block's rows are consecutive, kThreads / lanes of them for each u.
+template <int E>
+__device__ __forceinline__ unsigned row_of(const KvRows& P, int u) {
+  const unsigned per = (unsigned)kThreads >> P.lanes_log2;
+  return (unsigned)min((uint64_t)P.rows, ((uint64_t)blockIdx.x * kRowsPerThread + u) * per + (threadIdx.x >> P.lanes_log2));
+}
+
 // Sets err_flags of the requests this block looks after: whether a slot is outside [-1, num_slots).
 __device__ void check_slots(const KvRows& P) {
   if (!P.err_flags) return;
@@ -134,102 +143,148 @@ __device__ void check_slots(const KvRows& P) {
   }
 }
 
-// QUANT: the cache is e4m3; otherwise rows are copied bit for bit.
-template <typename T, bool QUANT>
+// E: elements of a row per lane.  QUANT: the cache is e4m3; otherwise rows are copied bit for bit.
+template <typename T, int E, bool QUANT>
 __global__ void __launch_bounds__(kThreads) kv_write_kernel(const KvRows P) {
-  constexpr int VB = Vec8<T>::kBytes;
+  constexpr int S = Vec8<T>::kBytes / 8;  // bytes of an element
   const unsigned lanes = 1u << P.lanes_log2;
-  const unsigned row = (unsigned)(((uint64_t)blockIdx.x * kThreads + threadIdx.x) >> P.lanes_log2);
-  const int e0 = (int)(threadIdx.x & (lanes - 1)) * kElems;
-  if (row < P.rows) {  // a row's lanes stay together: rows never straddle warps
+  const int e0 = (int)(threadIdx.x & (lanes - 1)) * E;
+  const bool in = e0 < P.D;
+  const unsigned char* src[kRowsPerThread];
+  size_t at[kRowsPerThread];  // the row's first element in the cache
+  int kv[kRowsPerThread];     // 0 K, 1 V, -1 nothing to write
+  float x[kRowsPerThread][E];
+#pragma unroll
+  for (int u = 0; u < kRowsPerThread; ++u) {
+    const unsigned row = row_of<E>(P, u);
+    kv[u] = -1;
+    if (row >= P.rows) continue;  // rows never straddle warps: a row's lanes stay together
     const unsigned n = specv::fdiv(row, P.fd_2h);
     int h = (int)(row - n * P.fd_2h.d);
-    const int kv = h >= P.H ? 1 : 0;
-    h -= kv ? P.H : 0;
     const long long slot = __ldg(P.slots + n);
-    const bool has = slot >= 0 && slot < P.num_slots;
-    if (has) {
-      const bool in = e0 < P.D;
-      const unsigned char* src = P.src[kv] + (long long)n * P.stride[kv] + ((size_t)h * P.D + e0) * (VB / kElems);
-      const size_t at = ((size_t)slot * P.H + h) * P.D + e0;  // element in the cache
-      if constexpr (QUANT) {
-        float x[kElems];
+    if (slot < 0 || slot >= P.num_slots) continue;
+    kv[u] = h >= P.H ? 1 : 0;
+    h -= kv[u] ? P.H : 0;
+    src[u] = P.src[kv[u]] + (long long)n * P.stride[kv[u]] + ((size_t)h * P.D + e0) * S;
+    at[u] = ((size_t)slot * P.H + h) * P.D;
+    if (QUANT) {
 #pragma unroll
-        for (int i = 0; i < kElems; ++i) x[i] = 0.f;
-        if (in) Vec8<T>::load(src, x);
-        float a = 0.f;
+      for (int i = 0; i < E; i += 8) {
+        float(&y)[8] = reinterpret_cast<float(&)[8]>(x[u][i]);
 #pragma unroll
-        for (int i = 0; i < kElems; ++i) {
-          const float m = fabsf(x[i]);
-          a = fmaxf(a, m < INFINITY ? m : 0.f);
-        }
-        const unsigned group = (lanes == 32 ? 0xffffffffu : ((1u << lanes) - 1u)) << ((threadIdx.x & 31) & ~(lanes - 1));
-        for (unsigned o = lanes >> 1; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(group, a, o));
-        const int e = scale_exponent(a);
-        const float inv = pow2f_int(-e);
-        uint32_t c[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float lo = x[2 * i] * inv, hi = x[2 * i + 1] * inv;
-          lo = fabsf(lo) <= 448.f ? lo : NAN;  // infinities (finite elements are within 448)
-          hi = fabsf(hi) <= 448.f ? hi : NAN;
-          c[i] = e4m3x2(lo, hi);
-        }
-        if (in) *reinterpret_cast<uint2*>(P.dst[kv] + at) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-        if (e0 == 0) P.scale_out[kv][(size_t)slot * P.H + h] = pow2f_int(e);
-      } else if (in) {
-        const uint4* s = reinterpret_cast<const uint4*>(src);
-        uint4* d = reinterpret_cast<uint4*>(P.dst[kv] + at * (VB / kElems));
-#pragma unroll
-        for (int i = 0; i < VB / 16; ++i) d[i] = __ldcs(s + i);
+        for (int z = 0; z < 8; ++z) y[z] = 0.f;
+        if (in) Vec8<T>::load(src[u] + i * S, y);
       }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kRowsPerThread; ++u) {
+    if (kv[u] < 0) continue;
+    if constexpr (QUANT) {
+      float a = 0.f;
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const float m = fabsf(x[u][i]);
+        a = fmaxf(a, m < INFINITY ? m : 0.f);
+      }
+      const unsigned group = (lanes == 32 ? 0xffffffffu : ((1u << lanes) - 1u)) << ((threadIdx.x & 31) & ~(lanes - 1));
+      for (unsigned o = lanes >> 1; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(group, a, o));
+      const int e = scale_exponent(a);
+      const float inv = pow2f_int(-e);
+      uint32_t c[E / 4];
+#pragma unroll
+      for (int i = 0; i < E / 4; ++i) {
+        float y[4];
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          y[z] = x[u][4 * i + z] * inv;
+          y[z] = fabsf(y[z]) <= 448.f ? y[z] : NAN;  // infinities (finite elements are within 448)
+        }
+        c[i] = e4m3x2(y[0], y[1]) | (e4m3x2(y[2], y[3]) << 16);
+      }
+      if (in) {
+        unsigned char* dst = P.dst[kv[u]] + at[u] + e0;
+        if constexpr (E == 16)
+          *reinterpret_cast<uint4*>(dst) = make_uint4(c[0], c[1], c[2], c[3]);
+        else
+          *reinterpret_cast<uint2*>(dst) = make_uint2(c[0], c[1]);
+      }
+      if (e0 == 0) P.scale_out[kv[u]][at[u] / P.D] = pow2f_int(e);
+    } else if (in) {
+      const uint4* s = reinterpret_cast<const uint4*>(src[u]);
+      uint4* d = reinterpret_cast<uint4*>(P.dst[kv[u]] + (at[u] + e0) * S);
+#pragma unroll
+      for (int i = 0; i < E * S / 16; ++i) d[i] = __ldcs(s + i);
     }
   }
   check_slots(P);
 }
 
-template <typename T, bool QUANT>
+template <typename T, int E, bool QUANT>
 __global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvRows P) {
-  constexpr int VB = Vec8<T>::kBytes;
+  constexpr int S = Vec8<T>::kBytes / 8;
+  constexpr int W = QUANT ? E / 4 : E * S / 4;  // words a lane reads
   const unsigned lanes = 1u << P.lanes_log2;
-  const unsigned row = (unsigned)(((uint64_t)blockIdx.x * kThreads + threadIdx.x) >> P.lanes_log2);
-  const int e0 = (int)(threadIdx.x & (lanes - 1)) * kElems;
-  if (row < P.rows && e0 < P.D) {
+  const int e0 = (int)(threadIdx.x & (lanes - 1)) * E;
+  unsigned char* dst[kRowsPerThread];
+  bool does[kRowsPerThread];
+  uint32_t w[kRowsPerThread][W];
+  float scale[kRowsPerThread];
+#pragma unroll
+  for (int u = 0; u < kRowsPerThread; ++u) {
+    const unsigned row = row_of<E>(P, u);
+    does[u] = row < P.rows && e0 < P.D;
+    scale[u] = 0.f;
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[u][i] = 0;
+    if (!does[u]) continue;
     const unsigned n = specv::fdiv(row, P.fd_2h);
     int h = (int)(row - n * P.fd_2h.d);
     const int kv = h >= P.H ? 1 : 0;
     h -= kv ? P.H : 0;
+    dst[u] = P.dst[kv] + (((size_t)n * P.H + h) * P.D + e0) * S;
     const long long slot = __ldg(P.slots + n);
-    const bool has = slot >= 0 && slot < P.num_slots;
-    unsigned char* dst = P.dst[kv] + (((size_t)n * P.H + h) * P.D + e0) * (VB / kElems);
-    const size_t at = has ? ((size_t)slot * P.H + h) * P.D + e0 : 0;
-    if constexpr (QUANT) {
-      float x[kElems];
-#pragma unroll
-      for (int i = 0; i < kElems; ++i) x[i] = 0.f;
-      if (has) {
-        const uint2 c = __ldcs(reinterpret_cast<const uint2*>(P.src[kv] + at));
-        const float s = __ldg(P.scale_in[kv] + (size_t)slot * P.H + h);
-        const uint32_t w[2] = {c.x, c.y};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = from_e4m3x2(w[i >> 1] >> (16 * (i & 1)));
-          x[2 * i] = f.x * s;
-          x[2 * i + 1] = f.y * s;
-        }
-      }
-      Vec8<T>::store(dst, x);
+    if (slot < 0 || slot >= P.num_slots) continue;
+    const size_t r = (size_t)slot * P.H + h;
+    const unsigned char* src = P.src[kv] + (r * P.D + e0) * (QUANT ? 1 : S);
+    if constexpr (W == 2) {
+      const uint2 v = __ldcs(reinterpret_cast<const uint2*>(src));
+      w[u][0] = v.x, w[u][1] = v.y;
     } else {
-      const uint4* s = reinterpret_cast<const uint4*>(P.src[kv] + at * (VB / kElems));
-      uint4* d = reinterpret_cast<uint4*>(dst);
 #pragma unroll
-      for (int i = 0; i < VB / 16; ++i) d[i] = has ? __ldcs(s + i) : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < W / 4; ++i) {
+        const uint4 v = __ldcs(reinterpret_cast<const uint4*>(src) + i);
+        w[u][4 * i] = v.x, w[u][4 * i + 1] = v.y, w[u][4 * i + 2] = v.z, w[u][4 * i + 3] = v.w;
+      }
+    }
+    if (QUANT) scale[u] = __ldg(P.scale_in[kv] + r);
+  }
+#pragma unroll
+  for (int u = 0; u < kRowsPerThread; ++u) {
+    if (!does[u]) continue;
+    if constexpr (QUANT) {
+#pragma unroll
+      for (int i = 0; i < E; i += 8) {
+        float x[8];
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          const float2 f = from_e4m3x2(w[u][i / 4 + z / 2] >> (16 * (z & 1)));
+          x[2 * z] = f.x * scale[u];
+          x[2 * z + 1] = f.y * scale[u];
+        }
+        Vec8<T>::store(dst[u] + i * S, x);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < W / 4; ++i)
+        reinterpret_cast<uint4*>(dst[u])[i] = make_uint4(w[u][4 * i], w[u][4 * i + 1], w[u][4 * i + 2], w[u][4 * i + 3]);
     }
   }
   check_slots(P);
 }
 
 int elem_bytes(spec_dtype_t t) { return t == SPEC_DTYPE_F32 ? 4 : t == SPEC_DTYPE_E4M3 ? 1 : 2; }
+int lane_elems(int D) { return D % 16 == 0 ? 16 : 8; }
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 // Checks shared by both calls; `done`: nothing to do.
@@ -240,7 +295,7 @@ spec_status_t plan(KvRows& P, spec_dtype_t dtype, spec_dtype_t cache, int B, int
   if (dtype != SPEC_DTYPE_F32 && dtype != SPEC_DTYPE_BF16 && dtype != SPEC_DTYPE_F16) return SPEC_ERR_INVALID_ARG;
   if (cache != dtype && cache != SPEC_DTYPE_E4M3) return SPEC_ERR_INVALID_ARG;
   if (B < 0 || T < 0 || H < 1 || D < 1 || num_slots < 0) return SPEC_ERR_INVALID_ARG;
-  if (D % kElems != 0 || D > SPEC_MAX_KV_HEAD_DIM) return SPEC_ERR_UNSUPPORTED;
+  if (D % 8 != 0 || D > SPEC_MAX_KV_HEAD_DIM) return SPEC_ERR_UNSUPPORTED;
   if (num_slots > INT_MAX) return SPEC_ERR_UNSUPPORTED;  // a slot is an int32
   const long long tokens = (long long)B * T;
   if (H > (INT_MAX / 2) || tokens > INT_MAX || tokens * 2 * H > INT_MAX) return SPEC_ERR_UNSUPPORTED;
@@ -266,14 +321,44 @@ spec_status_t plan(KvRows& P, spec_dtype_t dtype, spec_dtype_t cache, int B, int
   P.H = H;
   P.D = D;
   P.lanes_log2 = 0;
-  while ((kElems << P.lanes_log2) < D) ++P.lanes_log2;
+  while ((lane_elems(D) << P.lanes_log2) < D) ++P.lanes_log2;
   P.fd_2h = specv::make_fastdiv((unsigned)(2 * H));
   return SPEC_OK;
 }
 
 unsigned grid_of(const KvRows& P) {
-  const uint64_t blocks = (((uint64_t)P.rows << P.lanes_log2) + kThreads - 1) / kThreads;
-  return blocks ? (unsigned)blocks : 1u;  // at most 2^31 * 32 / 256
+  const uint64_t per = ((uint64_t)kThreads >> P.lanes_log2) * kRowsPerThread;
+  const uint64_t blocks = (P.rows + per - 1) / per;
+  return blocks ? (unsigned)blocks : 1u;
+}
+
+// One of the two kernels, for elements of type T.
+template <typename T, bool WRITE, bool QUANT>
+void launch(const KvRows& P, cudaStream_t s) {
+  const unsigned grid = grid_of(P);
+  if (lane_elems(P.D) == 16) {
+    if (WRITE)
+      kv_write_kernel<T, 16, QUANT><<<grid, kThreads, 0, s>>>(P);
+    else
+      kv_read_kernel<T, 16, QUANT><<<grid, kThreads, 0, s>>>(P);
+  } else {
+    if (WRITE)
+      kv_write_kernel<T, 8, QUANT><<<grid, kThreads, 0, s>>>(P);
+    else
+      kv_read_kernel<T, 8, QUANT><<<grid, kThreads, 0, s>>>(P);
+  }
+}
+template <bool WRITE>
+spec_status_t launch_any(const KvRows& P, spec_dtype_t dtype, bool quant, cudaStream_t s) {
+  if (dtype == SPEC_DTYPE_F32)
+    quant ? launch<float, WRITE, true>(P, s) : launch<float, WRITE, false>(P, s);
+  else if (dtype == SPEC_DTYPE_BF16 && quant)
+    launch<__nv_bfloat16, WRITE, true>(P, s);
+  else if (quant)
+    launch<__half, WRITE, true>(P, s);
+  else  // 16-bit rows are copied whatever they hold
+    launch<__half, WRITE, false>(P, s);
+  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
 }  // namespace
@@ -301,18 +386,7 @@ extern "C" spec_status_t spec_kv_write(const void* k, const void* v, spec_dtype_
   P.scale_out[1] = v_scale;
   P.stride[0] = k_stride * S;
   P.stride[1] = v_stride * S;
-  const unsigned grid = grid_of(P);
-  const cudaStream_t st_ = reinterpret_cast<cudaStream_t>(stream);
-  const bool q = cache_dtype == SPEC_DTYPE_E4M3;
-  if (dtype == SPEC_DTYPE_F32)
-    q ? kv_write_kernel<float, true><<<grid, kThreads, 0, st_>>>(P) : kv_write_kernel<float, false><<<grid, kThreads, 0, st_>>>(P);
-  else if (dtype == SPEC_DTYPE_BF16 && q)
-    kv_write_kernel<__nv_bfloat16, true><<<grid, kThreads, 0, st_>>>(P);
-  else if (q)
-    kv_write_kernel<__half, true><<<grid, kThreads, 0, st_>>>(P);
-  else  // 16-bit rows are copied whatever they hold
-    kv_write_kernel<__half, false><<<grid, kThreads, 0, st_>>>(P);
-  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+  return launch_any<true>(P, dtype, cache_dtype == SPEC_DTYPE_E4M3, reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" spec_status_t spec_kv_read(const void* k_cache, const void* v_cache, spec_dtype_t cache_dtype,
@@ -330,16 +404,5 @@ extern "C" spec_status_t spec_kv_read(const void* k_cache, const void* v_cache, 
   P.dst[1] = static_cast<unsigned char*>(v_out);
   P.scale_in[0] = k_scale;
   P.scale_in[1] = v_scale;
-  const unsigned grid = grid_of(P);
-  const cudaStream_t st_ = reinterpret_cast<cudaStream_t>(stream);
-  const bool q = cache_dtype == SPEC_DTYPE_E4M3;
-  if (dtype == SPEC_DTYPE_F32)
-    q ? kv_read_kernel<float, true><<<grid, kThreads, 0, st_>>>(P) : kv_read_kernel<float, false><<<grid, kThreads, 0, st_>>>(P);
-  else if (dtype == SPEC_DTYPE_BF16 && q)
-    kv_read_kernel<__nv_bfloat16, true><<<grid, kThreads, 0, st_>>>(P);
-  else if (q)
-    kv_read_kernel<__half, true><<<grid, kThreads, 0, st_>>>(P);
-  else
-    kv_read_kernel<__half, false><<<grid, kThreads, 0, st_>>>(P);
-  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+  return launch_any<false>(P, dtype, cache_dtype == SPEC_DTYPE_E4M3, reinterpret_cast<cudaStream_t>(stream));
 }
