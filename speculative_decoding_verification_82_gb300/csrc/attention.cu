@@ -186,7 +186,9 @@ extern "C" spec_status_t spec_attention(const void* q, spec_dtype_t dtype, long 
   A.out = static_cast<unsigned char*>(out);
   A.lse = lse;
   A.err_flags = err_flags;
-  const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
+  int ctas = sms < kMaxCtas ? sms : kMaxCtas;
+  A.lanes = (A.nqp == 2 || A.nqp == 4) && ctas >= A.nqp ? A.nqp : 1;
+  ctas -= ctas % A.lanes;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool pair = UR > kTile;
   const cudaError_t e = bf16 ? specv::attn::launch_attention<__nv_bfloat16>(A, head_dim, e4m3, pair, ctas, s)

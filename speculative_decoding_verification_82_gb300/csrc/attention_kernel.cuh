@@ -20,7 +20,9 @@
 //
 // Work.  The tiles of all (request, row tile, KV head) items in sequence are cut into equal ranges, one
 // per CTA, so ragged lengths and few requests still fill every SM.  Ends of ranges that fall inside an
-// item leave partial results (O, m, l) in the workspace, which attention_combine_kernel joins.
+// item leave partial results (O, m, l) in the workspace, which attention_combine_kernel joins.  Where a request
+// has two or four row units, as many CTAs side by side take the same range of tiles for one unit each (a lane
+// each), so that all but one read K and V from L2.
 //
 // Roles.  Warps 0-3 and 4-7: softmax of stream 0 and 1, a thread per row.  Warp 8: one lane issues the
 // products of both streams in turn (the tensor cores run them in that order, which the places that scores
@@ -49,7 +51,7 @@ constexpr float kGrow = 8.f;     // how far (log2) the maximum may outgrow m bef
 
 struct Record {  // an item whose tiles several CTAs share: it starts in the CTA that writes the record
   int b, qp, h;  // b < 0: none
-  int last;      // the last CTA with a part of it
+  int last;      // the last CTA with a part of it (every P.lanes-th from this one on)
 };
 
 struct Params {
@@ -66,6 +68,7 @@ struct Params {
   long long q_stride, num_pages;
   int B, T, Hq, H, G, P, page_log2;
   int nqp;         // row units (pair: 256 rows, split: 128) of a request with T tokens
+  int lanes;       // 1, or nqp: CTA c works on units c % lanes alone
   int q_box;       // tokens of qmap's box, 0: query rows are gathered by loads
   FastDiv fd_g, fd_nqp;
   float c;         // scale * log2(e)
@@ -298,8 +301,12 @@ struct SegIter {
         off = 0;
         if (++h == P.H) h = 0;
       }
-      if (nt == 0 || h == 0)
-        if (++qp == P.nqp) qp = 0, ++b;
+      if (nt == 0 || h == 0) {
+        if (P.lanes > 1)
+          ++b;
+        else if (++qp == P.nqp)
+          qp = 0, ++b;
+      }
       if (nt > 0) return true;
     }
     return false;
@@ -373,14 +380,17 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
   }
   if (warp == 8) tc_alloc(tmem_at);
   {
-    const int U = P.B * P.nqp;  // (at most INT_MAX)
+    // units of this CTA's lane: all (b, qp) in sequence, or (b, lane)
+    const int step = P.lanes > 1 ? 1 : P.nqp, lane_qp = P.lanes > 1 ? (int)(blockIdx.x % P.lanes) : 0;
+    const int U = P.B * step;  // (at most INT_MAX)
+    const int ctas = gridDim.x / P.lanes, cta = blockIdx.x / P.lanes;
     const int each = (int)(((unsigned)U + C::kThreads - 1) / C::kThreads);
     const int ua = (int)min((long long)U, (long long)each * tid), ub = (int)min((long long)U, (long long)ua + each);
-    const int b0 = (int)fdiv((unsigned)ua, P.fd_nqp), qp0 = ua - b0 * P.nqp;
+    const int b0 = P.lanes > 1 ? ua : (int)fdiv((unsigned)ua, P.fd_nqp), qp0 = P.lanes > 1 ? 0 : ua - b0 * P.nqp;
     long long sum = 0;
     for (int u = ua, b = b0, qp = qp0; u < ub; ++u) {
-      sum += (long long)unit_tiles<UR>(P, request_lens(P, b), qp) * P.H;
-      if (++qp == P.nqp) qp = 0, ++b;
+      sum += (long long)unit_tiles<UR>(P, request_lens(P, b), lane_qp + qp) * P.H;
+      if (++qp == step) qp = 0, ++b;
     }
     long long incl = sum;
     for (int o = 1; o < 32; o <<= 1) {
@@ -395,19 +405,19 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
       before += w < warp ? scan[w] : 0;
       total += scan[w];
     }
-    const long long per = max(1LL, (total + gridDim.x - 1) / gridDim.x);
-    const long long start = min(total, per * blockIdx.x), end = min(total, start + per);
+    const long long per = max(1LL, (total + ctas - 1) / ctas);
+    const long long start = min(total, per * cta), end = min(total, start + per);
     long long at = before + incl - sum;
     const bool has_start = start < end && start >= at && start < at + sum;
     const bool has_end = start < end && end < total && end >= at && end < at + sum;
     if (has_start || has_end)
       for (int u = ua, b = b0, qp = qp0; u < ub; ++u) {
-        const int nt = unit_tiles<UR>(P, request_lens(P, b), qp);
+        const int nt = unit_tiles<UR>(P, request_lens(P, b), lane_qp + qp);
         const long long next = at + (long long)nt * P.H;
         if (has_start && start >= at && start < next) {
           plan.take = end - start;
           plan.b = b;
-          plan.qp = qp;
+          plan.qp = lane_qp + qp;
           plan.h = (int)((start - at) / nt);
           plan.off = (int)((start - at) % nt);
         }
@@ -416,13 +426,13 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
           const long long item = at + (long long)h * nt;
           if (item >= start && item < end) {  // it starts here and goes on
             Record r;
-            r.b = b, r.qp = qp, r.h = h;
-            r.last = (int)((item + nt - 1) / per);
+            r.b = b, r.qp = lane_qp + qp, r.h = h;
+            r.last = (int)((item + nt - 1) / per) * P.lanes + lane_qp;
             P.rec[blockIdx.x] = r;
           }
         }
         at = next;
-        if (++qp == P.nqp) qp = 0, ++b;
+        if (++qp == step) qp = 0, ++b;
       }
   }
   tc_fence_before();
@@ -521,8 +531,22 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
         const int i = PAIR ? k : 2 * k + s;  // the segment's tile
         const int j0 = (g.nt - 1 - (g.off + i)) * kTile;
         const bool masked = j0 + kTile > all;
+        // The V that the products take after this softmax is waited for by its first warp, where possible while the
+        // scores are still to come, so that issuing has one wait for both.  (Stream 1's products follow stream
+        // 0's: in pair, stream 0 waits for both.  A split stream's first V, and any V that a warpgroup of its own
+        // converts, only once the tile's K is known to be there.  Before, the tile ahead of V in its slot might
+        // be missing too, and a wait two phases ahead ends at once.)
+        auto wait_v = [&] {
+          if ((warp & 3) != 0 || (PAIR && s == 1)) return;
+          const uint32_t vseq = 2 * kv + v_at(g, i);
+          ok = mbar_wait_warp(full + vseq % NS, (vseq / NS) & 1, abort);
+        };
+        const bool early = !E4M3 && (PAIR || k > 0);
+        if (early) wait_v();
+        if (!ok) break;
         ok = mbar_wait_warp(s_full + s, ph_s, abort);
         ph_s ^= 1;
+        if (ok && !early) wait_v();
         if (!ok) break;
         tc_fence_after();
         uint32_t seen[4] = {0, 0, 0, 0};  // a masked tile's positions that the row sees
@@ -671,7 +695,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
             for (int x = 0; x < C::kHalves; ++x)
 #pragma unroll
               for (int y = 0; y < 8; ++y) {
-                const uint4 v = lds128_at(at + x * C::kHalfBytes + y * 16);
+                const uint4 v = lds128_at(at + x * C::kHalfBytes + ((y ^ (row & 7)) << 4));  // (any order: no bank twice)
                 constexpr uint32_t E = Half<OT>::kExp * 0x10001u, one = (0x8000u - Half<OT>::kExp) * 0x10001u;
                 bad |= ((v.x & E) + one) | ((v.y & E) + one) | ((v.z & E) + one) | ((v.w & E) + one);
               }
@@ -680,7 +704,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
 #pragma unroll
               for (int x = 0; x < C::kHalves; ++x)
 #pragma unroll
-                for (int y = 0; y < 8; ++y) sts128(at + x * C::kHalfBytes + y * 16, 0, 0, 0, 0);
+                for (int y = 0; y < 8; ++y) sts128(at + x * C::kHalfBytes + ((y ^ (row & 7)) << 4), 0, 0, 0, 0);
             }
             const uint32_t w = __ballot_sync(kFull, nan);
             if (lane == 0) poison[mi * 4 + (warp & 3)] = w;
@@ -833,24 +857,16 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
         __syncwarp();
       };
       // O of stream s from its k-th tile, then S of its next, with nothing in between where that K is in place
-      // (pair: waited for; split: the V slot may be what its load waits for)
-      auto step = [&](int s, int k) {
+      // (V is; see the softmax warps).  Issuing ends as the products run out, so what lies between two
+      // steps leaves the tensor cores idle: one wait, and slots that are counted on, not divided for.
+      auto step = [&](int s, int k, uint32_t vslot, uint32_t kslot, uint32_t kpar) {
         const bool more = k + 1 < (s ? cnt1 : cnt0);
-        const uint32_t vseq = 2 * kv + v_at(g, PAIR ? k : 2 * k + s), vslot = vseq % NS;
-        const uint32_t kseq = 2 * kv + k_at(PAIR ? k + 1 : 2 * k + 2 + s), kslot = kseq % NS;
         const uint64_t v = tile_desc(sbase + C::kKv + vslot * C::kTileBytes, C::kHalfBytes);
-        ok = ok && mbar_wait_warp(full + vslot, (vseq / NS) & 1, abort);
-        bool next = false;
-        if (more && ok) {
-          if (PAIR)
-            next = ok = mbar_wait_warp(full + kslot, (kseq / NS) & 1, abort);
-          else
-            next = __all_sync(kFull, mbar_test_wait(full + kslot, (kseq / NS) & 1));
-        }
         ok = ok && mbar_wait_warp(p_ready + s, (ph_p >> s) & 1, abort);
         ph_p ^= 1u << s;
         if (!ok) return;
         tc_fence_after();
+        const bool next = more && __all_sync(kFull, mbar_test_wait(full + kslot, kpar));
         if (lead) {
 #pragma unroll
           for (int x = 0; x < kTile / 16; ++x) tc_mma_ts(col_o(s), col_s(s) + 8 * x, v + ((x * 2048) >> 4), id_pv, k > 0 || x > 0);
@@ -863,9 +879,20 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
       };
       qk(0, 0);
       if (cnt1 > 0) qk(1, 0);
+      // the slots of V(i) and of the K taken after it (pair: K(i + 1), split: K(i + 2)), and that K's parity
+      uint32_t vs = (2 * kv + 2) % NS, ks = (2 * kv + (PAIR ? 1 : 3)) % NS, kp = ((2 * kv + (PAIR ? 1 : 3)) / NS) & 1;
+      auto last_v = [&](int i, uint32_t slot) { return i + 1 < g.take ? slot : slot == 0 ? NS - 1u : slot - 1u; };
+      auto advance = [&] {
+        vs += 2;
+        vs -= vs >= NS ? NS : 0;
+        ks += 2;
+        if (ks >= NS) ks -= NS, kp ^= 1;
+      };
       for (int k = 0; ok && k < cnt0; ++k) {
-        step(0, k);
-        if (k < cnt1) step(1, k);
+        step(0, k, last_v(PAIR ? k : 2 * k, vs), ks, kp);
+        if (!PAIR) advance();
+        if (k < cnt1) step(1, k, last_v(PAIR ? k : 2 * k + 1, vs), ks, kp);
+        advance();
       }
       if (ok && lead) tc_commit(q_empty + qb);
       __syncwarp();
@@ -936,7 +963,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
   } else if (warp == 10) {
     // ======================================================================= queries ====
     const int ql = lane;
-    int last = -1;  // the last segment whose queries were asked for
+    int last = -1;               // the last segment whose queries were asked for
+    int tree_of[2] = {-1, -1};   // the requests whose parents the buffers hold
     SegIter<UR> it(plan);
     Seg g;
     for (int seg = 0; ok && it.next(P, g); ++seg) {
@@ -1024,7 +1052,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
         }
         landing = 0;
       }
-      if (P.parents) {
+      if (P.parents && g.b != tree_of[qb]) {  // (the heads and row units of a request follow one another)
+        tree_of[qb] = g.b;
         Parent* pr = par + (PAIR ? 0 : qb * kTile);
         bool bad = false;
         for (int i = lane; i < g.n; i += 32) {
@@ -1154,13 +1183,13 @@ __global__ void __launch_bounds__(256) attention_combine_kernel(const __grid_con
   if (row >= rows) return;
   const float2* ml = P.part_ml + row;
   float M = -INFINITY;
-  for (int x = c; x <= rec.last; ++x) M = fmaxf(M, ml[(size_t)(2 * x + (x == c)) * UR].x);
+  for (int x = c; x <= rec.last; x += P.lanes) M = fmaxf(M, ml[(size_t)(2 * x + (x == c)) * UR].x);
   const int r = rec.qp * UR + row, t = r / P.G;
   const size_t orow = ((size_t)rec.b * P.T + t) * P.Hq + rec.h * P.G + (r - t * P.G);
   for (int q4 = threadIdx.x >> 4; q4 < D / 4; q4 += 16) {
     float l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int x = c; x <= rec.last; ++x) {
+    for (int x = c; x <= rec.last; x += P.lanes) {
       const size_t slot = 2 * x + (x == c);
       const float2 v = ml[slot * UR];
       const float w = v.x == -INFINITY ? 0.f : ex2(v.x - M);
