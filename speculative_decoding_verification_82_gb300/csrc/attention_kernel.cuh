@@ -26,9 +26,10 @@
 //
 // Roles.  Warps 0-3 and 4-7: softmax of stream 0 and 1, a thread per row.  Warp 8: one lane issues the
 // products of both streams in turn (the tensor cores run them in that order, which the places that scores
-// and weights share rely on).  Warp 9: TMA loads of K and V pages into a ring of tiles.  Warp 10: query
-// rows and tree parents.  Warps 11-14 and 15-18 (e4m3): K and V codes to 16 bits.  Every wait is bounded:
-// one that gives up sets the CTA's abort flag, every role leaves, copies and products in flight are waited
+// and weights share rely on).  Warps 9 and 11: TMA loads of K and V pages into a ring of tiles, each every
+// second box (a lane takes about 54 cycles to issue one: with 16-position pages, one warp's 860 a tile held
+// up the products: 64 chains over 4096 positions: 164 -> 151 us).  Warp 10: query rows and tree parents.  Warps
+// 12-15 and 16-19 (e4m3): K and V codes to 16 bits.  Every wait is bounded: one that gives up sets the CTA's abort flag, every role leaves, copies and products in flight are waited
 // for, and the requests get SPEC_ERRF_TIMEOUT.
 #pragma once
 
@@ -97,7 +98,7 @@ struct Cfg {
   static constexpr int kMlAt = kQexpAt + (E4M3 ? 2 * kTile : 0);          // split: a float2 a row
   static constexpr int kBars = kMlAt + (PAIR ? 0 : kTile * 8);
   static constexpr int kBytes = kBars + 560;
-  static constexpr int kConvert = 11;                      // the first of the warps that convert codes (8 of them)
+  static constexpr int kConvert = 12;                      // the first of the warps that convert codes (8 of them)
   static constexpr int kThreads = (kConvert + (E4M3 ? 8 : 0)) * 32;
   static_assert(kBytes <= 232448 && kBars % 16 == 0, "shared memory");
   static_assert(kRaw <= kSlots, "see the converters");
@@ -356,11 +357,11 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
   // -- set-up, and this CTA's range of the tile sequence
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
-      mbar_init(full + i, E4M3 ? 4 : 1);
+      mbar_init(full + i, E4M3 ? 4 : 2);
       mbar_init(empty + i, 1);
     }
     for (int i = 0; i < NR; ++i) {
-      mbar_init(raw_full + i, 1);
+      mbar_init(raw_full + i, 2);
       mbar_init(raw_empty + i, 4);
     }
     for (int i = 0; i < 2; ++i) {
@@ -502,8 +503,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
     uint32_t ph_mark = 0;  // bit i: parity of mark[i]
     uint32_t kv = 0;              // KV tiles before this segment
     SegIter<UR> it(plan);
-    Seg g;
-    for (int seg = 0; ok && it.next(P, g); ++seg) {
+    Seg g, coming;
+    bool more = it.next(P, g);
+    for (int seg = 0; ok && more; ++seg, g = coming) {
       const int cnt = stream_tiles(g, s), cnt1 = s == 1 ? cnt : stream_tiles(g, 1);
       const int r0 = g.qp * UR + (PAIR ? s * kTile : 0);  // (a unit's rows fit an int: T G <= INT_MAX)
       const int rows = g.n * P.G;
@@ -531,22 +533,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
         const int i = PAIR ? k : 2 * k + s;  // the segment's tile
         const int j0 = (g.nt - 1 - (g.off + i)) * kTile;
         const bool masked = j0 + kTile > all;
-        // The V that the products take after this softmax is waited for by its first warp, where possible while the
-        // scores are still to come, so that issuing has one wait for both.  (Stream 1's products follow stream
-        // 0's: in pair, stream 0 waits for both.  A split stream's first V, and any V that a warpgroup of its own
-        // converts, only once the tile's K is known to be there.  Before, the tile ahead of V in its slot might
-        // be missing too, and a wait two phases ahead ends at once.)
-        auto wait_v = [&] {
-          if ((warp & 3) != 0 || (PAIR && s == 1)) return;
-          const uint32_t vseq = 2 * kv + v_at(g, i);
-          ok = mbar_wait_warp(full + vseq % NS, (vseq / NS) & 1, abort);
-        };
-        const bool early = !E4M3 && (PAIR || k > 0);
-        if (early) wait_v();
-        if (!ok) break;
+        const uint32_t vseq = 2 * kv + v_at(g, i), vslot = vseq % NS, vpar = (vseq / NS) & 1;
         ok = mbar_wait_warp(s_full + s, ph_s, abort);
         ph_s ^= 1;
-        if (ok && !early) wait_v();
         if (!ok) break;
         tc_fence_after();
         uint32_t seen[4] = {0, 0, 0, 0};  // a masked tile's positions that the row sees
@@ -685,10 +674,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
           const int mi = PAIR ? k & 7 : 4 * s + (k & 3);
           uint64_t* mb = mark + mi;
           if (!PAIR || s == 0) {
-            const uint32_t seq = 2 * kv + v_at(g, i), slot = seq % NS;
-            ok = mbar_wait_warp(full + slot, (seq / NS) & 1, abort);
+            ok = mbar_wait_warp(full + vslot, vpar, abort);
             if (!ok) break;
-            const uint32_t at = sbase + C::kKv + slot * C::kTileBytes + row * 128;
+            const uint32_t at = sbase + C::kKv + vslot * C::kTileBytes + row * 128;
             const bool hide = j0 + row >= stop;
             uint32_t bad = 0;  // the top bit of a half is set when its exponent is all ones
 #pragma unroll
@@ -717,11 +705,18 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
           const uint32_t* bad = poison + mi * 4;
           if ((bad[0] & seen[0]) | (bad[1] & seen[1]) | (bad[2] & seen[2]) | (bad[3] & seen[3])) l = NAN;
         }
+        // V is in place when the weights are said to be, so that issuing has one wait for both.  (Stream 1's
+        // products follow stream 0's: in pair, stream 0 waits for both.)
+        if ((warp & 3) == 0 && (!PAIR || s == 0)) {
+          ok = mbar_wait_warp(full + vslot, vpar, abort);
+          if (!ok) break;
+        }
         tc_fence_before();
         mbar_arrive_warp(p_ready + s);
       }
       // the segment's parents (and, with the products', its queries) may be replaced
       mbar_arrive_warp(q_empty + qb);
+      more = it.next(P, coming);  // (its lengths are read while the last products run)
       if (ok && cnt > 0) {
         ok = mbar_wait_warp(o_full + s, ph_o, abort);
         ph_o ^= 1;
@@ -908,7 +903,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
       }
       __syncwarp();
     }
-  } else if (warp == 9) {
+  } else if (warp == 9 || warp == 11) {
     // ========================================================================= loads ====
     constexpr int N = E4M3 ? NR : NS;              // the ring that copies land in
     constexpr int kBoxes = E4M3 ? 1 : C::kHalves;  // column boxes of a row
@@ -918,8 +913,10 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
     const uint32_t ring = sbase + (E4M3 ? C::kRawAt : C::kKv);
     const int box_log2 = P.page_log2 < 7 ? P.page_log2 : 7;  // rows of a box
     const int pieces = kTile >> box_log2;
-    const int piece = lane / kBoxes, col = lane % kBoxes;
-    const bool mine = piece < pieces;  // (at most 16 pieces of 2 boxes)
+    // this lane's box of a tile (at most 16 pieces of 2 boxes, every second one this warp's), and the warp's bytes
+    const int which = warp == 9 ? 0 : 1, box = 2 * lane + which, piece = box / kBoxes, col = box % kBoxes;
+    const bool mine = piece < pieces;
+    const uint32_t bytes = (uint32_t)(pieces * kBoxes + 1 - which) / 2 * (kStage / (uint32_t)(pieces * kBoxes));
     uint32_t seq = 0;  // (2^31 tiles a CTA are out of reach)
     SegIter<UR> it(plan);
     Seg g;
@@ -937,7 +934,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
         const uint32_t slot = seq % N;
         if (seq >= N) ok = mbar_wait_warp(eb + slot, (seq / N - 1) & 1, abort);
         if (!ok) return;
-        if (lane == 0) mbar_arrive_expect(fb + slot, kStage);
+        if (lane == 0) mbar_arrive_expect(fb + slot, bytes);
         __syncwarp();
         if (mine)
           tma_load_4d(ring + slot * kStage + col * C::kHalfBytes + ((uint32_t)piece << box_log2) * (E4M3 ? D : 128),
