@@ -85,7 +85,7 @@ struct Cfg {
   static constexpr int kRaw = E4M3 ? (D == 64 ? 6 : PAIR ? 3 : 4) : 0;
   static constexpr int kSlots = E4M3 ? (D == 64 ? 6 : PAIR ? 3 : 4) : (D == 64 ? 10 : PAIR ? 5 : 6);
   // The ring's order is K(0), K(1), V(0), K(2), V(1), ...: a tile's V is wanted a softmax later than its K.
-  // The exponents of a tile's scales are written with its K and kept as long as its softmax is due.  The streams
+  // What the softmax takes of a tile's scales is written with its K and kept as long as its softmax is due.  The streams
   // may drift apart, but by no more than the raw ring is long: its copies are in sequence, and one whose slot is
   // taken stops it.  So no tile 8 or more ahead is converted meanwhile.
   static constexpr int kScales = E4M3 ? 8 : 0;
@@ -94,7 +94,7 @@ struct Cfg {
   static constexpr int kRawAt = kKv + kSlots * kTileBytes;
   static constexpr int kParAt = kRawAt + kRaw * kRawBytes;  // parents: 16 bits each (pair), 2 x 128 bytes (split)
   static constexpr int kScaleAt = kParAt + (PAIR ? 2 * kMaxTree : 2 * kTile);
-  static constexpr int kQexpAt = kScaleAt + kScales * 32;  // exponents of the query rows' scales
+  static constexpr int kQexpAt = kScaleAt + kScales * 48;  // exponents of the query rows' scales
   static constexpr int kMlAt = kQexpAt + (E4M3 ? 2 * kTile : 0);          // split: a float2 a row
   static constexpr int kBars = kMlAt + (PAIR ? 0 : kTile * 8);
   static constexpr int kBytes = kBars + 560;
@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
   using Parent = typename std::conditional<PAIR, uint16_t, uint8_t>::type;   // (split: at most 128 tokens)
   constexpr Parent kNoParent = (Parent)~(Parent)0;
   Parent* par = reinterpret_cast<Parent*>(smem + C::kParAt);                // pair [kMaxTree], split [2][128]
-  int* exps = reinterpret_cast<int*>(smem + C::kScaleAt);                   // [kScales][K, V][4]: see the converters
+  float* exps = reinterpret_cast<float*>(smem + C::kScaleAt);               // [kScales][2^k, v, 2^-v][4]: see the converters
   uint8_t* qexp = smem + C::kQexpAt;                                        // pair [256], split [2][128]
   constexpr int ES = C::kScales > 0 ? C::kScales : 1;
   using OT = typename std::conditional<E4M3, __half, T>::type;              // the products' operands
@@ -527,8 +527,10 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
       float m = -INFINITY, l = 0.f;
       ok = mbar_wait_warp(q_full + qb, (uint32_t)((seg / qbufs) & 1), abort);  // parents are in place
       const bool bad_tree = ok && P.parents && tree_bad[qb];
-      // e4m3: scores come in units of the row's query scale (a power of two; see the query warps)
-      const int qe = E4M3 && !std::is_same<T, __half>::value ? (int)qexp[PAIR ? s * kTile + row : qb * kTile + row] - 127 : 0;
+      // e4m3: scores come in units of the row's query scale (a power of two; see the query warp)
+      float cq = P.c;
+      if constexpr (E4M3 && !std::is_same<T, __half>::value)
+        cq *= __uint_as_float((uint32_t)qexp[PAIR ? s * kTile + row : qb * kTile + row] << 23);
       for (int k = 0; ok && k < cnt; ++k) {
         const int i = PAIR ? k : 2 * k + s;  // the segment's tile
         const int j0 = (g.nt - 1 - (g.off + i)) * kTile;
@@ -579,19 +581,15 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
           }
         }
         if (warp_live) {
-          // e4m3: exponents of the tile's scales, by 32 positions
-          int4 ke4 = make_int4(0, 0, 0, 0), ve4 = ke4;
+          // Scores to log2 units (c > 0).  e4m3: positions 32 w on are in units of 2^k[w], their V rows in units of
+          // 2^v[w].
+          float4 k4 = make_float4(0.f, 0.f, 0.f, 0.f), v4 = k4, i4 = k4;
           if constexpr (E4M3) {
-            const int4* at = reinterpret_cast<const int4*>(exps + (kv + i) % ES * 8);
-            ke4 = at[0];
-            ve4 = at[1];
+            const float4* at = reinterpret_cast<const float4*>(exps + (kv + i) % ES * 12);
+            k4 = at[0], v4 = at[1], i4 = at[2];
           }
-          const int ke[4] = {ke4.x, ke4.y, ke4.z, ke4.w}, ve[4] = {ve4.x, ve4.y, ve4.z, ve4.w};
-          // scores to log2 units: of positions 32 w on (c > 0)
-          auto factor = [&](int w) {
-            if constexpr (!E4M3) return P.c;
-            return P.c * __uint_as_float((uint32_t)max(1, min(254, qe + ke[w] + 127)) << 23);
-          };
+          const float cs[4] = {E4M3 ? cq * k4.x : P.c, E4M3 ? cq * k4.y : P.c, E4M3 ? cq * k4.z : P.c, E4M3 ? cq * k4.w : P.c};
+          const float ve[4] = {v4.x, v4.y, v4.z, v4.w}, vi[4] = {i4.x, i4.y, i4.z, i4.w};
           // Two passes over the scores, 32 at a time, the next ones on their way: the maximum, then the
           // weights, which take the place of scores already read.
           uint32_t x[2][16];
@@ -609,7 +607,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
               m1 = fmaxf(m1, __uint_as_float(y[j + 1]));
             }
             if constexpr (E4M3)
-              top = fmaxf(top, fmaf(fmaxf(m0, m1), factor(w / 2), (float)ve[w / 2]));
+              top = fmaxf(top, fmaf(fmaxf(m0, m1), cs[w / 2], ve[w / 2]));
             else
               top = fmaxf(top, fmaxf(m0, m1) * P.c);
           }
@@ -645,7 +643,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
             tc_wait_ld();
             if (w < 7) tc_ld16(S + 16 * (w + 1), x[(w + 1) & 1]);
             const uint32_t* y = x[w & 1];
-            const float c = factor(w / 2), up = E4M3 ? mm + (float)ve[w / 2] : mm;
+            const float c = cs[w / 2], up = E4M3 ? mm + ve[w / 2] : mm;
             const float2 c2 = make_float2(c, c), m2 = make_float2(up, up);
             float2 s0 = make_float2(0.f, 0.f), s1 = s0;
             uint32_t p[8];
@@ -661,8 +659,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
             }
             tc_st8(S + 8 * w, p);
             float sum = (s0.x + s0.y) + (s1.x + s1.y);
-            if constexpr (E4M3) sum *= __uint_as_float((uint32_t)(127 - ve[w / 2]) << 23);
-            l += sum;
+            l = E4M3 ? fmaf(sum, vi[w / 2], l) : l + sum;
           }
           tc_wait_st();
         }
@@ -1018,34 +1015,39 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
         if (!ok) break;
         // bf16 to f16 in place: a power of two brings the row's largest finite magnitude to 2^14 .. 2^15, so
         // that only elements below 2^-38 of it lose bits
-        for (int r = ql; r < rows; r += 32) {
+        constexpr int N = V / 4;  // 16-byte vectors of one of a row's four lanes
+        for (int r = ql / 4; r < (rows + 7) / 8 * 8; r += 8) {  // (all lanes stay: their maxima are exchanged)
           const uint32_t at = qat + (r / kTile) * qbytes + (r % kTile) * 128;
+          uint4 v[N];
           uint32_t top = 0;
-#pragma unroll 4
-          for (int y = 0; y < V; ++y) {
-            const uint4 v = lds128_at(at + (y / 8) * qhalf + (y % 8) * 16);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int y = 0; y < N; ++y) {
+            const int c = N * (ql & 3) + y;
+            v[y] = lds128_at(at + (c / 8) * qhalf + (c % 8) * 16);
+            const uint32_t w[4] = {v[y].x, v[y].y, v[y].z, v[y].w};
 #pragma unroll
             for (int z = 0; z < 4; ++z) {
               const uint32_t lo = (w[z] >> 7) & 0xffu, hi = (w[z] >> 23) & 0xffu;  // exponents
               top = max(top, max(lo == 255u ? 0u : lo, hi == 255u ? 0u : hi));
             }
           }
+          top = max(top, __shfl_xor_sync(kFull, top, 1));
+          top = max(top, __shfl_xor_sync(kFull, top, 2));
           const uint32_t e = max(top, 15u);  // the row in units of 2^(e - 141)
           const float f = __uint_as_float((268u - e) << 23);
-#pragma unroll 4
-          for (int y = 0; y < V; ++y) {
-            const uint32_t a = at + (y / 8) * qhalf + (y % 8) * 16;
-            const uint4 v = lds128_at(a);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          if (r >= rows) continue;
+#pragma unroll
+          for (int y = 0; y < N; ++y) {
+            const int c = N * (ql & 3) + y;
+            const uint32_t w[4] = {v[y].x, v[y].y, v[y].z, v[y].w};
             uint32_t o[4];
 #pragma unroll
             for (int z = 0; z < 4; ++z)
               o[z] = Half<__half>::pack(__uint_as_float(w[z] << 16) * f, __uint_as_float(w[z] & 0xffff0000u) * f);
-            sts128(a, o[0], o[1], o[2], o[3]);
+            sts128(at + (c / 8) * qhalf + (c % 8) * 16, o[0], o[1], o[2], o[3]);
           }
           // the factor back is 2^(e - 141); its float exponent e - 14 is at least 1
-          qexp[PAIR ? r : qb * kTile + r] = (uint8_t)(e - 14);
+          if ((ql & 3) == 0) qexp[PAIR ? r : qb * kTile + r] = (uint8_t)(e - 14);
         }
         landing = 0;
       }
@@ -1127,9 +1129,10 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
           const int ve = max(-60, min(100, exponent(now.y)));
           const int e = v ? ve : max(-126, exponent(now.x));
           if (!v && lane == 0) {
-            int* at = exps + (kv + i) % ES * 8 + cw;
-            at[0] = e;
-            at[4] = ve;
+            float* at = exps + (kv + i) % ES * 12 + cw;
+            at[0] = __uint_as_float((uint32_t)(e + 127) << 23);
+            at[4] = (float)ve;
+            at[8] = __uint_as_float((uint32_t)(127 - ve) << 23);
           }
           const __half2 rel = __float2half2_rn((v ? now.y : now.x) * __uint_as_float((uint32_t)(127 - e) << 23));
 #pragma unroll
