@@ -29,8 +29,9 @@
 // and weights share rely on).  Warps 9 and 11: TMA loads of K and V pages into a ring of tiles, each every
 // second box (a lane takes about 54 cycles to issue one: with 16-position pages, one warp's 860 a tile held
 // up the products: 64 chains over 4096 positions: 164 -> 151 us).  Warp 10: query rows and tree parents.  Warps
-// 12-15 and 16-19 (e4m3): K and V codes to 16 bits.  Every wait is bounded: one that gives up sets the CTA's abort flag, every role leaves, copies and products in flight are waited
-// for, and the requests get SPEC_ERRF_TIMEOUT.
+// 12-15 and 16-19 (e4m3): K and V codes to 16 bits.  Every wait is bounded: one that gives up sets the CTA's
+// abort flag, every role leaves, copies and products in flight are waited for, and the requests get
+// SPEC_ERRF_TIMEOUT.
 #pragma once
 
 #include <cuda.h>
@@ -100,6 +101,9 @@ struct Cfg {
   static constexpr int kBytes = kBars + 560;
   static constexpr int kConvert = 12;                      // the first of the warps that convert codes (8 of them)
   static constexpr int kThreads = (kConvert + (E4M3 ? 8 : 0)) * 32;
+  static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;  // registers a thread at launch
+  static constexpr int kMoreRegs = E4M3 ? 120 : 192, kLessRegs = E4M3 ? 80 : 120;
+  static_assert(8 * kMoreRegs + (kThreads / 32 - 8) * kLessRegs <= kThreads / 32 * kLaunchRegs, "registers");
   static_assert(kBytes <= 232448 && kBars % 16 == 0, "shared memory");
   static_assert(kRaw <= kSlots, "see the converters");
 };
@@ -174,6 +178,20 @@ __device__ __forceinline__ void tc_st16(uint32_t t, const uint32_t* r) {
       "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(t)
       : "memory");
+}
+template <int W>
+__device__ __forceinline__ void tc_ld_cols(uint32_t t, uint32_t* r) {
+  if constexpr (W == 32)
+    tc_ld32(t, r);
+  else
+    tc_ld16(t, r);
+}
+template <int W>
+__device__ __forceinline__ void tc_st_cols(uint32_t t, const uint32_t* r) {
+  if constexpr (W == 32)
+    tc_st32(t, r);
+  else
+    tc_st16(t, r);
 }
 // Two 32-bit operations in one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
@@ -460,6 +478,11 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
   const int qbytes = qhalf * C::kHalves;                                           // and of a row tile
   bool ok = true;  // no wait gave up
 
+  // The softmax warps take registers over from the others, each group of four warps alike; the launch's total stays.
+  if (warp < 8)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kMoreRegs));
+  else
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kLessRegs));
   if (warp < 8) {
     // ======================================================================= softmax ====
     const int s = warp >> 2, row = tid & 127;
@@ -499,6 +522,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
         }
       }
     }
+    // Registers: what spills goes to an L1 that shared memory leaves little of, at L2's latency (e4m3 with 50 words of it:
+    // every role ran at half its pace).  With 120 a thread columns come 16 at a time and loops are unrolled in part.
+    constexpr int kSteps = E4M3 ? 2 : 4, W = E4M3 ? 16 : 32;
     uint32_t ph_s = 0, ph_o = 0, ph_join = 0;  // parities of s_full, o_full, join
     uint32_t ph_mark = 0;  // bit i: parity of mark[i]
     uint32_t kv = 0;              // KV tiles before this segment
@@ -566,16 +592,17 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
           // what it does not see becomes -inf in place
           if (warp_live) {
 #pragma unroll 1
-            for (int w = 0; w < 4; ++w) {
-              const uint32_t bits = w == 0 ? seen[0] : w == 1 ? seen[1] : w == 2 ? seen[2] : seen[3];
+            for (int w = 0; w < kTile; w += W) {
+              uint32_t bits = w < 32 ? seen[0] : w < 64 ? seen[1] : w < 96 ? seen[2] : seen[3];
+              if constexpr (W == 16) bits = bits >> (w & 16) & 0xffffu;
               __syncwarp();
-              if (__all_sync(kFull, bits == ~0u)) continue;
-              uint32_t x[32];
-              tc_ld32(S + 32 * w, x);
+              if (__all_sync(kFull, bits == (W == 16 ? 0xffffu : ~0u))) continue;
+              uint32_t x[W];
+              tc_ld_cols<W>(S + w, x);
               tc_wait_ld();
 #pragma unroll
-              for (int j = 0; j < 32; ++j) x[j] = bits & (1u << j) ? x[j] : 0xff800000u;
-              tc_st32(S + 32 * w, x);
+              for (int j = 0; j < W; ++j) x[j] = bits & (1u << j) ? x[j] : 0xff800000u;
+              tc_st_cols<W>(S + w, x);
             }
             tc_wait_st();
           }
@@ -583,33 +610,32 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
         if (warp_live) {
           // Scores to log2 units (c > 0).  e4m3: positions 32 w on are in units of 2^k[w], their V rows in units of
           // 2^v[w].
-          float4 k4 = make_float4(0.f, 0.f, 0.f, 0.f), v4 = k4, i4 = k4;
-          if constexpr (E4M3) {
-            const float4* at = reinterpret_cast<const float4*>(exps + (kv + i) % ES * 12);
-            k4 = at[0], v4 = at[1], i4 = at[2];
-          }
-          const float cs[4] = {E4M3 ? cq * k4.x : P.c, E4M3 ? cq * k4.y : P.c, E4M3 ? cq * k4.z : P.c, E4M3 ? cq * k4.w : P.c};
-          const float ve[4] = {v4.x, v4.y, v4.z, v4.w}, vi[4] = {i4.x, i4.y, i4.z, i4.w};
+          const float* sc = exps + (E4M3 ? (kv + i) % ES * 12 : 0);
           // Two passes over the scores, 32 at a time, the next ones on their way: the maximum, then the
           // weights, which take the place of scores already read.
           uint32_t x[2][16];
           float top = -INFINITY;
           tc_ld16(S, x[0]);
+#pragma unroll kSteps
+          for (int w = 0; w < 4; ++w) {
+            float most = -INFINITY;
 #pragma unroll
-          for (int w = 0; w < 8; ++w) {
-            tc_wait_ld();
-            tc_ld16(S + (w < 7 ? 16 * (w + 1) : 0), x[(w + 1) & 1]);
-            const uint32_t* y = x[w & 1];
-            float m0 = __uint_as_float(y[0]), m1 = __uint_as_float(y[1]);
+            for (int z = 0; z < 2; ++z) {
+              tc_wait_ld();
+              tc_ld16(S + (w < 3 || z == 0 ? 32 * w + 16 * z + 16 : 0), x[1 - z]);
+              const uint32_t* y = x[z];
+              float m0 = __uint_as_float(y[0]), m1 = __uint_as_float(y[1]);
 #pragma unroll
-            for (int j = 2; j < 16; j += 2) {
-              m0 = fmaxf(m0, __uint_as_float(y[j]));
-              m1 = fmaxf(m1, __uint_as_float(y[j + 1]));
+              for (int j = 2; j < 16; j += 2) {
+                m0 = fmaxf(m0, __uint_as_float(y[j]));
+                m1 = fmaxf(m1, __uint_as_float(y[j + 1]));
+              }
+              most = fmaxf(most, fmaxf(m0, m1));
             }
             if constexpr (E4M3)
-              top = fmaxf(top, fmaf(fmaxf(m0, m1), cs[w / 2], ve[w / 2]));
+              top = fmaxf(top, fmaf(most, cq * sc[w], sc[4 + w]));
             else
-              top = fmaxf(top, fmaxf(m0, m1) * P.c);
+              top = fmaxf(top, most * P.c);
           }
           // f16 weights: 2^7 up, so that they stay below 2^15 after the growth allowed, and only those
           // below 2^-21 of the largest get subnormal
@@ -627,39 +653,42 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
               }
               tc_wait_ld();
 #pragma unroll 1
-              for (int w = 0; w < D / 32; ++w) {
-                uint32_t o[32];
-                tc_ld32(O + 32 * w, o);
+              for (int w = 0; w < D; w += W) {
+                uint32_t o[W];
+                tc_ld_cols<W>(O + w, o);
                 tc_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * a);
-                tc_st32(O + 32 * w, o);
+                for (int j = 0; j < W; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * a);
+                tc_st_cols<W>(O + w, o);
               }
             }
           }
           const float mm = m == -INFINITY ? 0.f : -m;
-#pragma unroll
-          for (int w = 0; w < 8; ++w) {
-            tc_wait_ld();
-            if (w < 7) tc_ld16(S + 16 * (w + 1), x[(w + 1) & 1]);
-            const uint32_t* y = x[w & 1];
-            const float c = cs[w / 2], up = E4M3 ? mm + ve[w / 2] : mm;
+#pragma unroll kSteps
+          for (int w = 0; w < 4; ++w) {
+            const float c = E4M3 ? cq * sc[w] : P.c, up = E4M3 ? mm + sc[4 + w] : mm;
             const float2 c2 = make_float2(c, c), m2 = make_float2(up, up);
             float2 s0 = make_float2(0.f, 0.f), s1 = s0;
-            uint32_t p[8];
 #pragma unroll
-            for (int j = 0; j < 16; j += 4) {
-              float2 a = fma2(make_float2(__uint_as_float(y[j]), __uint_as_float(y[j + 1])), c2, m2);
-              float2 b = fma2(make_float2(__uint_as_float(y[j + 2]), __uint_as_float(y[j + 3])), c2, m2);
-              a.x = ex2(a.x), a.y = ex2(a.y), b.x = ex2(b.x), b.y = ex2(b.y);
-              s0 = add2(s0, a);
-              s1 = add2(s1, b);
-              p[j / 2] = Half<OT>::pack(a.x, a.y);  // rounded to the type the product takes
-              p[j / 2 + 1] = Half<OT>::pack(b.x, b.y);
+            for (int z = 0; z < 2; ++z) {
+              tc_wait_ld();
+              if (w < 3 || z == 0) tc_ld16(S + 32 * w + 16 * z + 16, x[1 - z]);
+              const uint32_t* y = x[z];
+              uint32_t p[8];
+#pragma unroll
+              for (int j = 0; j < 16; j += 4) {
+                float2 a = fma2(make_float2(__uint_as_float(y[j]), __uint_as_float(y[j + 1])), c2, m2);
+                float2 b = fma2(make_float2(__uint_as_float(y[j + 2]), __uint_as_float(y[j + 3])), c2, m2);
+                a.x = ex2(a.x), a.y = ex2(a.y), b.x = ex2(b.x), b.y = ex2(b.y);
+                s0 = add2(s0, a);
+                s1 = add2(s1, b);
+                p[j / 2] = Half<OT>::pack(a.x, a.y);  // rounded to the type the product takes
+                p[j / 2 + 1] = Half<OT>::pack(b.x, b.y);
+              }
+              tc_st8(S + 16 * w + 8 * z, p);
             }
-            tc_st8(S + 8 * w, p);
-            float sum = (s0.x + s0.y) + (s1.x + s1.y);
-            l = E4M3 ? fmaf(sum, vi[w / 2], l) : l + sum;
+            const float sum = (s0.x + s0.y) + (s1.x + s1.y);
+            l = E4M3 ? fmaf(sum, sc[8 + w], l) : l + sum;
           }
           tc_wait_st();
         }
@@ -673,14 +702,14 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
           if (!PAIR || s == 0) {
             ok = mbar_wait_warp(full + vslot, vpar, abort);
             if (!ok) break;
-            const uint32_t at = sbase + C::kKv + vslot * C::kTileBytes + row * 128;
+            const uint32_t at = sbase + C::kKv + vslot * C::kTileBytes + row * 128 + ((row & 7) << 4);  // (its piece 0; piece y: at ^ (y << 4))
             const bool hide = j0 + row >= stop;
             uint32_t bad = 0;  // the top bit of a half is set when its exponent is all ones
 #pragma unroll
             for (int x = 0; x < C::kHalves; ++x)
 #pragma unroll
               for (int y = 0; y < 8; ++y) {
-                const uint4 v = lds128_at(at + x * C::kHalfBytes + ((y ^ (row & 7)) << 4));  // (any order: no bank twice)
+                const uint4 v = lds128_at((at ^ (y << 4)) + x * C::kHalfBytes);  // (any order: no bank twice)
                 constexpr uint32_t E = Half<OT>::kExp * 0x10001u, one = (0x8000u - Half<OT>::kExp) * 0x10001u;
                 bad |= ((v.x & E) + one) | ((v.y & E) + one) | ((v.z & E) + one) | ((v.w & E) + one);
               }
@@ -689,7 +718,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
 #pragma unroll
               for (int x = 0; x < C::kHalves; ++x)
 #pragma unroll
-                for (int y = 0; y < 8; ++y) sts128(at + x * C::kHalfBytes + ((y ^ (row & 7)) << 4), 0, 0, 0, 0);
+                for (int y = 0; y < 8; ++y) sts128((at ^ (y << 4)) + x * C::kHalfBytes, 0, 0, 0, 0);
             }
             const uint32_t w = __ballot_sync(kFull, nan);
             if (lane == 0) poison[mi * 4 + (warp & 3)] = w;
@@ -765,27 +794,27 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
         uint4* dst = reinterpret_cast<uint4*>(P.out + (orow * D + c0) * 2);
         float4* part = reinterpret_cast<float4*>(P.part_o) + ((size_t)slot * (D / 4) + c0 / 4) * UR + urow;
 #pragma unroll 1
-        for (int x = 0; x < (PAIR ? D / 32 : D / 64); ++x, dst += 4, part += 8 * UR) {
+        for (int x = 0; x < (PAIR ? D : D / 2); x += W, dst += W / 8, part += W / 4 * UR) {
           __syncwarp();
-          uint32_t o[32];
-          tc_ld32(col_o(PAIR ? s : 0) + lanes + c0 + 32 * x, o);
+          uint32_t o[W];
+          tc_ld_cols<W>(col_o(PAIR ? s : 0) + lanes + c0 + x, o);
           tc_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f0);
+          for (int j = 0; j < W; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f0);
           if (!PAIR && two) {
-            uint32_t o1[32];
-            tc_ld32(col_o(1) + lanes + c0 + 32 * x, o1);
+            uint32_t o1[W];
+            tc_ld_cols<W>(col_o(1) + lanes + c0 + x, o1);
             tc_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(fmaf(__uint_as_float(o1[j]), f1, __uint_as_float(o[j])));
+            for (int j = 0; j < W; ++j) o[j] = __float_as_uint(fmaf(__uint_as_float(o1[j]), f1, __uint_as_float(o[j])));
           }
           if (bad_tree) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = 0;
+            for (int j = 0; j < W; ++j) o[j] = 0;
           }
           if (live && whole) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < W / 8; ++j) {
               uint32_t w[4];
 #pragma unroll
               for (int z = 0; z < 4; ++z)
@@ -794,7 +823,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
             }
           } else if (live) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < W / 4; ++j)
               part[j * UR] = make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]),
                                          __uint_as_float(o[4 * j + 2]), __uint_as_float(o[4 * j + 3]));
           }
@@ -991,23 +1020,23 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
         int r = ql / V;
         int t = (int)fdiv((unsigned)(r0 + r), P.fd_g), gg = r0 + r - t * P.G;
         while (r < rows) {
-          uint4 x[8];
+          uint4 x[4];
           int n = 0;
 #pragma unroll
-          for (int u = 0; u < 8; ++u)
+          for (int u = 0; u < 4; ++u)
             if (r + u * R < rows) {
               x[u] = __ldg(reinterpret_cast<const uint4*>(q + (t * P.q_stride + (long long)gg * D) * 2));
               for (gg += R; gg >= P.G; gg -= P.G) ++t;
               n = u + 1;
             }
 #pragma unroll
-          for (int u = 0; u < 8; ++u)
+          for (int u = 0; u < 4; ++u)
             if (u < n) {
               const int rr = r + u * R, c = ql % V;
               sts128(qat + (rr / kTile) * qbytes + (c / 8) * qhalf + (rr % kTile) * 128 + (((c % 8) ^ (rr & 7)) << 4), x[u].x,
                      x[u].y, x[u].z, x[u].w);
             }
-          r += 8 * R;
+          r += 4 * R;
         }
         __syncwarp();
       }
@@ -1079,80 +1108,95 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
   } else {
     // ================================================================= codes to 16 bits ====
     if constexpr (E4M3) {
-      const int cw = warp - C::kConvert, row = (cw & 3) * 32 + lane, v = cw >= 4;  // four warps take the K tiles, four the V tiles
+      // Four warps take the K tiles, four the V tiles, 32 positions each.  Where no row behind the 64th lives, the live
+      // softmax warps are all in the first two quarters of the SM: then the two K warps of the other quarters take
+      // positions n and n + 64 each (64 chains of 6 tokens by 8 heads over 8192 positions: 252 -> 229 us; with 64
+      // columns, whose conversion is half as long, 206 -> 229, so not there).
+      const int cw = warp - C::kConvert, v = cw >= 4;
+      const bool half = D == 128 && !PAIR && !v && P.T * P.G <= kTile / 2;
+      const int unit = half ? (cw & 3) - 2 : cw & 3, row = unit * 32 + lane;
+      const int page_mask = (1 << P.page_log2) - 1;
+      const unsigned page_rows = (unsigned)P.H << P.page_log2;  // scales of a page
       uint32_t kv = 0;
       SegIter<UR> it(plan);
       Seg g;
-      while (ok && it.next(P, g)) {
+      while (unit >= 0 && ok && it.next(P, g)) {
         const int stop = g.L + g.n;
         const int32_t* table = P.table + (size_t)g.b * P.P;
-        // this thread's row of the segment's tile i: its page (-1: none), and its scales
-        auto page_of = [&](int i) {
-          const int j = (g.nt - 1 - (g.off + i)) * kTile + row;
-          return i < g.take && j < stop ? __ldg(table + (j >> P.page_log2)) : -1;
-        };
-        auto scales_of = [&](int i, int p) {
-          const int j = (g.nt - 1 - (g.off + i)) * kTile + row;
+        // the page of a row (-1: none), and its scales
+        auto page_of = [&](int j) { return j >= 0 && j < stop ? __ldg(table + (j >> P.page_log2)) : -1; };
+        auto scales_of = [&](int j, int p) {
           if (p < 0 || p >= P.num_pages) return make_float2(0.f, 0.f);
-          const size_t at = (((size_t)p << P.page_log2) + (j & ((1 << P.page_log2) - 1))) * P.H + g.h;
+          const unsigned long long at = (unsigned long long)(unsigned)p * page_rows + (unsigned)((j & page_mask) * P.H + g.h);
           return make_float2(v ? 0.f : __ldg(P.ks + at), __ldg(P.vs + at));
         };
-        // pages are fetched two tiles ahead, scales one
-        float2 now = scales_of(0, page_of(0));
-        int page = page_of(1);
-        for (int i = 0; ok && i < g.take; ++i) {
-          const float2 next = scales_of(i + 1, page);
-          page = page_of(i + 2);
+        // A scale goes with its codes in units of 2^e, e the exponent of the largest finite scale of its
+        // 32 rows (V: within the range that the weights' reference exponent covers).
+        auto exponent = [](float x) {
+          const uint32_t mag = __float_as_uint(fabsf(x));
+          return (int)(__reduce_max_sync(kFull, mag < 0x7f800000u ? mag : 0u) >> 23) - 127;
+        };
+        // pages are fetched two tiles ahead, scales one (behind the segment: unused)
+        int j = (g.nt - 1 - g.off) * kTile + row;
+        float2 now[2] = {scales_of(j, page_of(j)), make_float2(0.f, 0.f)};
+        int page[2] = {page_of(j - kTile), -1};
+        if (half) {
+          now[1] = scales_of(j + 64, page_of(j + 64));
+          page[1] = page_of(j + 64 - kTile);
+        }
+#pragma unroll 1
+        for (int i = 0; ok && i < g.take; ++i, j -= kTile) {
+          float2 next[2] = {scales_of(j - kTile, page[0]), make_float2(0.f, 0.f)};
+          page[0] = page_of(j - 2 * kTile);
+          if (half) {
+            next[1] = scales_of(j + 64 - kTile, page[1]);
+            page[1] = page_of(j + 64 - 2 * kTile);
+          }
           const uint32_t seq = 2 * kv + (v ? v_at(g, i) : k_at(i)), rs = seq % NR, slot = seq % NS;
           ok = mbar_wait_warp(raw_full + rs, (seq / NR) & 1, abort);
           // (Place seq - NS may be the other warpgroup's.  It has its slot: the raw ring is no longer than this
           // one, and a raw tile is given back only once its slot is had.  So at most one phase is to come.)
           if (ok && seq >= NS) ok = mbar_wait_warp(empty + slot, (seq / NS - 1) & 1, abort);
           if (!ok) break;
-          const uint32_t src = sbase + C::kRawAt + rs * C::kRawBytes + row * D;
-          const uint32_t dst = sbase + C::kKv + slot * C::kTileBytes + row * 128;
-          uint4 code[D / 16];
+          // Places of the row's 16-byte piece 0; piece y is at ^ (y << 4): pieces of a 128-byte row are exchanged by its
+          // row of 8, those of a 64-byte row by its pair of rows of 4 (the copy's and the products' swizzles)
+          uint32_t src = sbase + C::kRawAt + rs * C::kRawBytes + row * D + (D == 128 ? (row & 7) << 4 : ((row >> 1) & 3) << 4);
+          uint32_t dst = sbase + C::kKv + slot * C::kTileBytes + row * 128 + ((row & 7) << 4);
+#pragma unroll 1
+          for (int n = 0; n < (half ? 2 : 1); ++n, src += 64 * D, dst += 64 * 128) {
+            uint4 code[D / 16];
 #pragma unroll
-          for (int y = 0; y < D / 16; ++y) {
-            // the copy's swizzle: 16-byte pieces of a 128-byte row exchanged by its row of 8 (of a
-            // 64-byte row by its pair of rows of 4)
-            const int at = D == 128 ? (y ^ (row & 7)) : (y ^ ((row >> 1) & 3));
-            code[y] = lds128_at(src + (at << 4));
-          }
-          mbar_arrive_warp(raw_empty + rs);  // (its codes are in registers)
-          // a scale goes with its codes in units of 2^e, e the exponent of the largest finite scale of this
-          // warp's 32 rows (V: within the range that the weights' reference exponent covers)
-          auto exponent = [](float x) {
-            const uint32_t mag = __float_as_uint(fabsf(x));
-            return (int)(__reduce_max_sync(kFull, mag < 0x7f800000u ? mag : 0u) >> 23) - 127;
-          };
-          const int ve = max(-60, min(100, exponent(now.y)));
-          const int e = v ? ve : max(-126, exponent(now.x));
-          if (!v && lane == 0) {
-            float* at = exps + (kv + i) % ES * 12 + cw;
-            at[0] = __uint_as_float((uint32_t)(e + 127) << 23);
-            at[4] = (float)ve;
-            at[8] = __uint_as_float((uint32_t)(127 - ve) << 23);
-          }
-          const __half2 rel = __float2half2_rn((v ? now.y : now.x) * __uint_as_float((uint32_t)(127 - e) << 23));
-#pragma unroll
-          for (int y = 0; y < D / 16; ++y) {
-            const uint32_t w[4] = {code[y].x, code[y].y, code[y].z, code[y].w};
-            uint32_t o[8];
-#pragma unroll
-            for (int z = 0; z < 8; ++z) {
-              uint32_t h;
-              asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(w[z >> 1] >> (16 * (z & 1)))));
-              const __half2 f = __hmul2(*reinterpret_cast<const __half2*>(&h), rel);
-              o[z] = *reinterpret_cast<const uint32_t*>(&f);
+            for (int y = 0; y < D / 16; ++y) code[y] = lds128_at(src ^ (y << 4));
+            const int ve = max(-60, min(100, exponent(now[0].y)));
+            const int e = v ? ve : max(-126, exponent(now[0].x));
+            if (!v && lane == 0) {
+              float* at = exps + (kv + i) % ES * 12 + unit + 2 * n;
+              at[0] = __uint_as_float((uint32_t)(e + 127) << 23);
+              at[4] = (float)ve;
+              at[8] = __uint_as_float((uint32_t)(127 - ve) << 23);
             }
-            const int h = y / 4, c = 2 * (y % 4);
-            sts128(dst + h * C::kHalfBytes + ((c ^ (row & 7)) << 4), o[0], o[1], o[2], o[3]);
-            sts128(dst + h * C::kHalfBytes + (((c + 1) ^ (row & 7)) << 4), o[4], o[5], o[6], o[7]);
+            const __half2 rel = __float2half2_rn((v ? now[0].y : now[0].x) * __uint_as_float((uint32_t)(127 - e) << 23));
+            mbar_arrive_warp(raw_empty + rs);  // (its codes are in registers)
+#pragma unroll
+            for (int y = 0; y < D / 16; ++y) {
+              const uint32_t w[4] = {code[y].x, code[y].y, code[y].z, code[y].w};
+              uint32_t o[8];
+#pragma unroll
+              for (int z = 0; z < 8; ++z) {
+                uint32_t c;
+                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(c) : "h"((uint16_t)(w[z >> 1] >> (16 * (z & 1)))));
+                const __half2 f = __hmul2(*reinterpret_cast<const __half2*>(&c), rel);
+                o[z] = *reinterpret_cast<const uint32_t*>(&f);
+              }
+              const uint32_t at = (dst ^ ((y & 3) << 5)) + (y >> 2) * C::kHalfBytes;
+              sts128(at, o[0], o[1], o[2], o[3]);
+              sts128(at ^ 16, o[4], o[5], o[6], o[7]);
+            }
+            fence_proxy_async_shared();
+            mbar_arrive_warp(full + slot);
+            now[0] = now[1];
           }
-          fence_proxy_async_shared();
-          mbar_arrive_warp(full + slot);
-          now = next;
+          now[0] = next[0], now[1] = next[1];
         }
         kv += g.take;
       }
