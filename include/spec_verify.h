@@ -409,9 +409,12 @@ spec_status_t spec_kv_read(const void *k_cache, const void *v_cache, spec_dtype_
  * whole prefix and, in the chunk, to tokens 0..t (parents NULL) or to itself and its ancestors.
  *   out[b][t][h] = sum_j softmax_j(scale q . k_j) v_j
  * with the scores, the softmax statistics and the sums in 32 bits; the weights are rounded to
- * dtype before they multiply V (e4m3 caches: to f16, the V scales taken in; V scales of one request
- * should lie within 2^-60 .. 2^100, and a bf16 query's elements below 2^-38 of its largest are
- * rounded to that step), and the result is rounded once.
+ * dtype before they multiply V, and the result is rounded once.  e4m3 caches: K and V rows and the
+ * weights become f16, each row in units of the largest scale among its 32 positions (32 i ..
+ * 32 i + 31).  A scale that is a power of two, as spec_kv_write's are, loses nothing down to 2^-15
+ * of that largest; another one is rounded to f16's 11 bits, as is its product with a code.  V scales
+ * should lie within 2^-60 .. 2^100, and a bf16 query row's elements below 2^-38 of its largest are
+ * rounded to that step.
  *
  * q              token n = b T + t at q + n q_stride (elements; a 16-byte multiple, pointer
  *                16-byte aligned): num_heads rows of head_dim elements, bf16 or f16 (f32:
@@ -427,7 +430,7 @@ spec_status_t spec_kv_read(const void *k_cache, const void *v_cache, spec_dtype_
  * parents        [B][T] int32 or NULL, as for spec_verify_tree_greedy (checked over the request's
  *                chunk_len tokens): SPEC_ERRF_BAD_TREE.
  * scale          > 0 and finite.
- * out            [B][T][num_heads][head_dim] dtype, 16-byte aligned.
+ * out            [B][T][num_heads][head_dim] dtype, 16-byte aligned; overlaps no input.
  * lse            [B][T][num_heads] float or NULL: log sum_j exp(scale q . k_j).
  * err_flags      [B] int32 or NULL.  A request with a bad length or tree gets zeros (lse -inf).  A
  *                page outside [0, num_pages) sets SPEC_ERRF_BAD_SLOT; its rows are read as zeros.
@@ -436,7 +439,9 @@ spec_status_t spec_kv_read(const void *k_cache, const void *v_cache, spec_dtype_
  * other query.
  * workspace      spec_attention_workspace_bytes(...), 256-byte aligned; needs no initialisation and
  *                holds nothing between calls, but calls that may run concurrently need one each.
- * Limits: head_dim 64 or 128; page_size a power of two >= 8; T <= SPEC_MAX_WALK_NODES with parents.
+ * Limits (SPEC_ERR_UNSUPPORTED): head_dim 64 or 128; page_size a power of two >= 8; B <= 65535;
+ * T <= SPEC_MAX_WALK_NODES with parents; pages_per_request page_size and T (num_heads /
+ * num_kv_heads) at most INT_MAX / 2.
  */
 size_t spec_attention_workspace_bytes(int T, int num_heads, int num_kv_heads, int head_dim);
 spec_status_t spec_attention(const void *q, spec_dtype_t dtype, long long q_stride, int B, int T,

@@ -523,6 +523,6 @@ def spec_attention(q, k_cache, v_cache, page_table, context_len, *, chunk_len=No
     ef = _out(out.get("err_flags"), "err_flags", torch.int32, (B,), dev)
     _call(lib.spec_attention, dev, q, DTYPE_CODE[q.dtype], qs, B, T, Hq, H, D, k_cache, v_cache,
           CACHE_CODE[k_cache.dtype], k_scale, v_scale, k_cache.shape[0], k_cache.shape[1], page_table,
-          P, context_len, chunk_len, parents, D**-0.5 if scale is None else float(scale), o,
+          P, context_len, chunk_len, parents, max(D, 1) ** -0.5 if scale is None else float(scale), o,
           lse, ef, workspace, workspace.numel() * workspace.element_size())
     return dict(out=o, lse=lse, err_flags=ef)

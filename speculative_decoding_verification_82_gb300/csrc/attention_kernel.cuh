@@ -1168,7 +1168,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
 #pragma unroll
             for (int y = 0; y < D / 16; ++y) code[y] = lds128_at(src ^ (y << 4));
             const int ve = max(-60, min(100, exponent(now[0].y)));
-            const int e = v ? ve : max(-126, exponent(now[0].x));
+            const int e = v ? ve : max(-126, min(126, exponent(now[0].x)));
             if (!v && lane == 0) {
               float* at = exps + (kv + i) % ES * 12 + unit + 2 * n;
               at[0] = __uint_as_float((uint32_t)(e + 127) << 23);

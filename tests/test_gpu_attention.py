@@ -191,6 +191,47 @@ def test_against_the_definition(shape, kind):
     assert torch.equal(r["out"], call(c)["out"])  # the same bits again
 
 
+@pytest.mark.parametrize("T", [3, 40])
+@pytest.mark.parametrize("log2", [127, 126, -126])
+def test_scales_at_the_ends_of_their_range(T, log2):
+    """K scales next to float's largest and smallest powers of two, against queries that bring the scores back to
+    a few units.  (A score's factor, scale log2(e) 2^-126, may be subnormal: its 2^-21 of scores below 2^3 is
+    within what check allows.)"""
+    c = make(40, 2, T, 2, 8, 128, [300, 77], 16, e4m3=True)
+    g = gen(41)
+    codes = (torch.randn(c["k_cache"].shape, generator=g, device="cuda") * 2.0**-3).to(E4M3)
+    unused = c["k_cache"].view(torch.uint8) == 0x7F
+    c["k_cache"] = torch.where(unused, c["k_cache"].view(torch.uint8), codes.view(torch.uint8)).view(E4M3)
+    first = log2 - 2 if log2 > 0 else log2
+    c["k_scale"] = torch.exp2(torch.randint(first, first + 3, c["k_scale"].shape, generator=g, device="cuda").double()).float()
+    c["q"] = (torch.randn(c["q"].shape, generator=g, device="cuda").double() * 2.0 ** min(3 - log2, 124)).to(torch.bfloat16)
+    check(c, call(c))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("T", [2, 40])
+def test_scales_that_are_no_powers_of_two(T, D):
+    """Such a scale, relative to the largest of its 32 positions, is rounded to f16, and so is its product with a
+    code: a K or V element is off by d = (1 + 2^-11)^2 - 1 of itself.  Scores are then off by d sum |q k| scale at
+    most, weights by the exponential of twice that."""
+    c = make(42, 3, T, 2, 4, D, [500, 130, 3], 16, torch.float16, e4m3=True, sharp=0.02)
+    for name in ("k_scale", "v_scale"):
+        c[name] = c[name].clamp(2.0**-3, 1) * (1 + torch.rand(c[name].shape, generator=gen(43), device="cuda"))
+    r = call(c, lse=torch.zeros((3, T, 8), device="cuda"))
+    d = (1 + 2.0**-11) ** 2 - 1
+    u = torch.finfo(torch.float16).eps / 2
+    for b in range(3):
+        out, mag, lse, flat = reference(c, b)
+        k = (c["k_cache"].view(-1, 2, D).view(torch.uint8) & 0x7F).view(E4M3).double().nan_to_num(0) * c["k_scale"].view(-1, 2).double()[..., None]
+        at = torch.arange(int(c["context_len"][b]) + T, device="cuda")
+        k = k[c["page_table"][b].long()[at // 16] * 16 + at % 16]
+        q = c["q"][b].double().abs().view(T, 2, 4, D)
+        worst = torch.einsum("thgd,nhd->thgn", q, k).amax(-1).reshape(T, 8, 1) * D**-0.5 * d
+        tol = u * (1 + u) * out.abs() + (u + 2.0**-13 + torch.expm1(2 * worst) + d * torch.exp(2 * worst)) * mag + 2.0**-31 * flat + 2.0**-25
+        assert ((r["out"][b].double() - out).abs() <= tol).all()
+        assert ((r["lse"][b].double() - lse).abs() <= worst[..., 0] + 2.0**-13 * (1 + lse.abs())).all()
+
+
 @pytest.mark.parametrize("T,G,tree", [(6, 8, False), (61, 4, True), (300, 2, False)])
 def test_ragged_chunks_leave_the_rows_behind_them(T, G, tree):
     B = 5
@@ -444,3 +485,6 @@ def test_empty_calls():
     assert call(e)["out"].shape[0] == 0
     e = dict(c, q=c["q"][:, :0])
     assert call(e)["out"].shape[1] == 0
+    empty = [torch.empty(x.shape[:-1] + (0,), dtype=x.dtype, device="cuda") for x in (c["q"], c["k_cache"], c["v_cache"])]
+    with pytest.raises(binding.SpecVerifyError):
+        call(dict(c, q=empty[0], k_cache=empty[1], v_cache=empty[2]))
