@@ -409,7 +409,8 @@ spec_status_t spec_kv_read(const void *k_cache, const void *v_cache, spec_dtype_
  * whole prefix and, in the chunk, to tokens 0..t (parents NULL) or to itself and its ancestors.
  *   out[b][t][h] = sum_j softmax_j(scale q . k_j) v_j
  * with the scores, the softmax statistics and the sums in 32 bits; the weights are rounded to
- * dtype before they multiply V, and the result is rounded once.  e4m3 caches: K and V rows and the
+ * dtype before they multiply V, and the result is rounded once (bf16 V beyond 2^80 may overflow the
+ * sums).  e4m3 caches: K and V rows and the
  * weights become f16, each row in units of the largest scale among its 32 positions (32 i ..
  * 32 i + 31).  A scale that is a power of two, as spec_kv_write's are, loses nothing down to 2^-15
  * of that largest; another one is rounded to f16's 11 bits, as is its product with a code.  V scales

@@ -208,6 +208,23 @@ def test_scales_at_the_ends_of_their_range(T, log2):
     check(c, call(c))
 
 
+@pytest.mark.parametrize("T,G", [(2, 4), (40, 8)])
+def test_values_near_the_ends_of_their_range(T, G):
+    """bf16 V of 2^80 and of 2^-100, with scores that rise along the prefix's tiles in either direction by less and
+    by more than what is let pass without rescaling."""
+    for power in (80, -100):
+        for slope in (0.02, -0.02, 0.3, -0.3):
+            c = make(44, 2, T, 1, G, 64, [900, 100], 16)
+            c["v_cache"] = (c["v_cache"].double() * 2.0**power).to(torch.bfloat16)
+            at = torch.arange(1000, device="cuda")
+            for b in range(2):  # every query's first element is 1, the keys' grow along the positions
+                n = int(c["context_len"][b])
+                slot = c["page_table"][b].long()[at[:n] // 16] * 16 + at[:n] % 16
+                c["k_cache"].view(-1, 1, 64)[slot, 0, 0] = (slope * at[:n]).to(torch.bfloat16)
+            c["q"][..., 0] = 1.0
+            check(c, call(c))
+
+
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("T", [2, 40])
 def test_scales_that_are_no_powers_of_two(T, D):
