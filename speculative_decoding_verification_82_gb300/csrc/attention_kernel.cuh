@@ -860,8 +860,10 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
       const int qb = seg % qbufs;
       const int cnt0 = stream_tiles(g, 0), cnt1 = stream_tiles(g, 1);
       ok = mbar_wait_warp(q_full + qb, (uint32_t)((seg / qbufs) & 1), abort);
-      // S of stream s; the last reader of the K tile frees it
-      auto mma_qk = [&](int s, uint32_t slot) {
+      const int last_s = PAIR ? (cnt1 > 0 ? 1 : 0) : (g.take - 1) & 1, last_k = (last_s ? cnt1 : cnt0) - 1;
+      // S of stream s from its k-th tile; the last reader of the K tile frees it, and the segment's last one the queries,
+      // so that the next ones arrive while the last weights and sums are still at work
+      auto mma_qk = [&](int s, int k, uint32_t slot) {
         const uint64_t q = tile_desc(sbase + C::kQ + (PAIR ? s : qb) * qbytes, 16);
         const uint64_t b = tile_desc(sbase + C::kKv + slot * C::kTileBytes, 16);
 #pragma unroll
@@ -870,13 +872,14 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
                     id_qk, x > 0);
         tc_commit(s_full + s);
         if (!PAIR || s == 1 || cnt1 == 0) tc_commit(empty + slot);
+        if (s == last_s && k == last_k) tc_commit(q_empty + qb);
       };
       auto qk = [&](int s, int k) {  // from the stream's k-th tile
         const uint32_t seq = 2 * kv + k_at(PAIR ? k : 2 * k + s), slot = seq % NS;
         ok = ok && mbar_wait_warp(full + slot, (seq / NS) & 1, abort);
         if (!ok) return;
         tc_fence_after();
-        if (lead) mma_qk(s, slot);
+        if (lead) mma_qk(s, k, slot);
         __syncwarp();
       };
       // O of stream s from its k-th tile, then S of its next, with nothing in between where that K is in place
@@ -893,7 +896,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
         if (lead) {
 #pragma unroll
           for (int x = 0; x < kTile / 16; ++x) tc_mma_ts(col_o(s), col_s(s) + 8 * x, v + ((x * 2048) >> 4), id_pv, k > 0 || x > 0);
-          if (next) mma_qk(s, kslot);
+          if (next) mma_qk(s, k + 1, kslot);
           if (!PAIR || s == 1 || cnt1 == 0) tc_commit(empty + vslot);
           if (!more) tc_commit(o_full + s);
         }
@@ -917,8 +920,6 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
         if (k < cnt1) step(1, k, last_v(PAIR ? k : 2 * k + 1, vs), ks, kp);
         advance();
       }
-      if (ok && lead) tc_commit(q_empty + qb);
-      __syncwarp();
       kv += g.take;
     }
     if (!ok) {  // products in flight end before tensor memory is given back
@@ -1215,44 +1216,48 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
     for (int b = tid; b < P.B; b += C::kThreads) atomicOr(P.err_flags + b, SPEC_ERRF_TIMEOUT);
 }
 
-// Joins the parts of the items that several CTAs share.  Block (c, y): the item that starts in CTA c, 16 of
-// its rows; a thread takes four columns of a row (or fewer rows at a time for 64 columns).
+// Joins the parts of the items that several CTAs share.  Block (c, y): the item that starts in CTA c, 8 of its
+// rows (16 where a row has 64 columns); a thread takes four columns of a row.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) attention_combine_kernel(const __grid_constant__ Params P, int UR) {
+  constexpr int R = 1024 / D;  // rows of a block
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x;
   const Record rec = P.rec[c];
   if (rec.b < 0) return;
   const int n = P.chunk_len ? __ldg(P.chunk_len + rec.b) : P.T;
   const int rows = min((long long)UR, (long long)n * P.G - (long long)rec.qp * UR);
-  const int row = blockIdx.y * 16 + (threadIdx.x & 15);
+  const int row = blockIdx.y * R + threadIdx.x % R, q4 = threadIdx.x / R;
   if (row >= rows) return;
   const float2* ml = P.part_ml + row;
-  float M = -INFINITY;
-  for (int x = c; x <= rec.last; x += P.lanes) M = fmaxf(M, ml[(size_t)(2 * x + (x == c)) * UR].x);
+  const float4* po = reinterpret_cast<const float4*>(P.part_o) + (size_t)q4 * UR + row;
+  auto slot = [&](int x) { return (size_t)(2 * x + (x == c)); };
+  // the first two parts (most items have no more), then one at a time
+  const int second = c + P.lanes;
+  const float2 v0 = ml[slot(c) * UR], v1 = ml[slot(second) * UR];
+  const float4 p0 = po[slot(c) * (D / 4) * UR], p1 = po[slot(second) * (D / 4) * UR];
+  float M = fmaxf(v0.x, v1.x), l;
+  auto factor = [](float m, float M) { return m == -INFINITY ? 0.f : ex2(m - M); };
+  float w0 = factor(v0.x, M), w1 = factor(v1.x, M);
+  l = v0.y * w0 + v1.y * w1;
+  if (v0.y != v0.y || v1.y != v1.y) l = NAN;
+  float4 o = make_float4(fmaf(p1.x, w1, p0.x * w0), fmaf(p1.y, w1, p0.y * w0), fmaf(p1.z, w1, p0.z * w0), fmaf(p1.w, w1, p0.w * w0));
+  for (int x = second + P.lanes; x <= rec.last; x += P.lanes) {
+    const float2 v = ml[slot(x) * UR];
+    const float4 p = po[slot(x) * (D / 4) * UR];
+    const float N = fmaxf(M, v.x), a = factor(M, N), w = factor(v.x, N);
+    l = v.y == v.y ? fmaf(v.y, w, l * a) : NAN;
+    o = make_float4(fmaf(p.x, w, o.x * a), fmaf(p.y, w, o.y * a), fmaf(p.z, w, o.z * a), fmaf(p.w, w, o.w * a));
+    M = N;
+  }
   const int r = rec.qp * UR + row, t = r / P.G;
   const size_t orow = ((size_t)rec.b * P.T + t) * P.Hq + rec.h * P.G + (r - t * P.G);
-  for (int q4 = threadIdx.x >> 4; q4 < D / 4; q4 += 16) {
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int x = c; x <= rec.last; x += P.lanes) {
-      const size_t slot = 2 * x + (x == c);
-      const float2 v = ml[slot * UR];
-      const float w = v.x == -INFINITY ? 0.f : ex2(v.x - M);
-      const float4 p = reinterpret_cast<const float4*>(P.part_o)[(slot * (D / 4) + q4) * UR + row];
-      l = v.y == v.y ? fmaf(v.y, w, l) : NAN;
-      o.x = fmaf(p.x, w, o.x);
-      o.y = fmaf(p.y, w, o.y);
-      o.z = fmaf(p.z, w, o.z);
-      o.w = fmaf(p.w, w, o.w);
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    uint2 w2;
-    w2.x = Half<T>::pack(o.x * inv, o.y * inv);
-    w2.y = Half<T>::pack(o.z * inv, o.w * inv);
-    *reinterpret_cast<uint2*>(P.out + (orow * D + 4 * q4) * 2) = w2;
-    if (q4 == 0 && P.lse) P.lse[orow] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
-  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint2 w2;
+  w2.x = Half<T>::pack(o.x * inv, o.y * inv);
+  w2.y = Half<T>::pack(o.z * inv, o.w * inv);
+  *reinterpret_cast<uint2*>(P.out + (orow * D + 4 * q4) * 2) = w2;
+  if (q4 == 0 && P.lse) P.lse[orow] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
 }
 
 // Launches both kernels on `stream`.
@@ -1267,7 +1272,7 @@ cudaError_t launch_one(const Params& P, int ctas, cudaStream_t stream) {
   constexpr int UR = PAIR ? 2 * kTile : kTile;
   const long long rows = (long long)P.T * P.G < UR ? (long long)P.T * P.G : UR;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas, (unsigned)((rows + 15) / 16));
+  cfg.gridDim = dim3((unsigned)ctas, (unsigned)((rows + 1024 / D - 1) / (1024 / D)));
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
