@@ -13,6 +13,7 @@ import os
 from ctypes import c_float, c_int, c_size_t, c_void_p
 
 import torch
+from torch import Tensor
 
 from .build import LIB_PATH
 
@@ -100,9 +101,8 @@ def _stream(device) -> c_void_p:
 
 
 def _need(t, name: str, dtype, shape, device) -> torch.Tensor:
-    if (isinstance(t, torch.Tensor) and t.device == device and (dtype is None or t.dtype == dtype)
-            and t.shape == shape and t.is_contiguous()):
-        return t
+    if type(t) is Tensor and t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t  # (what a step calls with; the rest finds what is wrong)
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.device != device:
@@ -328,15 +328,22 @@ def spec_kv_compact(caches, slots, parents, accept_len, path_nodes, *, err_flags
     return ef
 
 
+# The current device, and a device's current stream as an address: what torch.cuda's functions of these names wrap
+# in objects, which would be a tenth of a small call's time on the host.
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
 def _call(fn, device, *args) -> None:
     """fn(*args, the current stream of `device`) with `device` current, its status checked.  Tensors among
     the arguments become their addresses."""
-    args = [a.data_ptr() if isinstance(a, torch.Tensor) else a for a in args]
-    if device.index == torch.cuda.current_device():
-        status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    args = [a.data_ptr() if type(a) is Tensor or isinstance(a, Tensor) else a for a in args]
+    index = device.index
+    if index == _current_device():
+        status = fn(*args, _current_stream(index))
     else:
         with torch.cuda.device(device):
-            status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+            status = fn(*args, _current_stream(index))
     if status != SPEC_OK:
         _check(status)
 
@@ -371,17 +378,24 @@ def spec_logits_process(logits, *, history=None, history_len=None, prompt_len=No
         _need(history_len, "history_len", i32, (B,), dev)
     elif history_len is not None or prompt_len is not None:
         raise ValueError("history_len and prompt_len need a history")
-    _opt(prompt_len, "prompt_len", i32, (B,), dev)
+    if prompt_len is not None:
+        _need(prompt_len, "prompt_len", i32, (B,), dev)
     if draft_tokens is not None and node_tokens is not None:
         raise ValueError("give draft_tokens (a chain) or node_tokens and parents (a tree), not both")
     if (node_tokens is None) != (parents is None):
         raise ValueError("node_tokens and parents go together")
-    _opt(draft_tokens, "draft_tokens", i32, (B, R - 1), dev)
-    _opt(node_tokens, "node_tokens", i32, (B, R), dev)
-    _opt(parents, "parents", i32, (B, R), dev)
-    _opt(repetition, "repetition", f32, (B,), dev)
-    _opt(presence, "presence", f32, (B,), dev)
-    _opt(frequency, "frequency", f32, (B,), dev)
+    if draft_tokens is not None:
+        _need(draft_tokens, "draft_tokens", i32, (B, R - 1), dev)
+    if node_tokens is not None:
+        _need(node_tokens, "node_tokens", i32, (B, R), dev)
+    if parents is not None:
+        _need(parents, "parents", i32, (B, R), dev)
+    if repetition is not None:
+        _need(repetition, "repetition", f32, (B,), dev)
+    if presence is not None:
+        _need(presence, "presence", f32, (B,), dev)
+    if frequency is not None:
+        _need(frequency, "frequency", f32, (B,), dev)
     nb = 0
     if (bias_tokens is None) != (bias_values is None):
         raise ValueError("bias_tokens and bias_values go together")
@@ -391,7 +405,8 @@ def spec_logits_process(logits, *, history=None, history_len=None, prompt_len=No
         nb = bias_tokens.shape[1]
         _need(bias_tokens, "bias_tokens", i32, (B, nb), dev)
         _need(bias_values, "bias_values", f32, (B, nb), dev)
-    _opt(allowed, "allowed", i32, (B, R, (V + 31) // 32), dev)
+    if allowed is not None:
+        _need(allowed, "allowed", i32, (B, R, (V + 31) // 32), dev)
     out = out or {}
     o = _out(out.get("logits"), "out logits", logits.dtype, (B, R, V), dev)
     ef = _out(out.get("err_flags"), "err_flags", i32, (B,), dev)
@@ -411,16 +426,16 @@ def _kv_caches(k_cache, v_cache, k_scale, v_scale, dtype, dev):
         raise ValueError("k_cache must be [num_slots][H][D] or [num_pages][page_size][H][D]")
     if k_cache.dtype not in (dtype, E4M3):
         raise TypeError(f"the caches must be {dtype} or {E4M3}, got {k_cache.dtype}")
-    _need(k_cache, "k_cache", None, k_cache.shape, dev)
-    _need(v_cache, "v_cache", k_cache.dtype, k_cache.shape, dev)
-    if k_cache.dtype == E4M3:
-        _need(k_scale, "k_scale", torch.float32, k_cache.shape[:-1], dev)
-        _need(v_scale, "v_scale", torch.float32, k_cache.shape[:-1], dev)
+    shape, code = k_cache.shape, k_cache.dtype
+    _need(k_cache, "k_cache", code, shape, dev)
+    _need(v_cache, "v_cache", code, shape, dev)
+    if code is E4M3:
+        rows = shape[:-1]
+        _need(k_scale, "k_scale", torch.float32, rows, dev)
+        _need(v_scale, "v_scale", torch.float32, rows, dev)
     elif k_scale is not None or v_scale is not None:
         raise ValueError("scales belong to e4m3 caches")
-    H, D = k_cache.shape[-2:]
-    slots = k_cache.shape[0] * (k_cache.shape[1] if k_cache.dim() == 4 else 1)
-    return slots, H, D
+    return shape[0] * shape[1] if len(shape) == 4 else shape[0], shape[-2], shape[-1]
 
 
 def _token_stride(t, name: str, B: int, T: int, H: int, D: int, dev) -> int:
@@ -511,9 +526,12 @@ def spec_attention(q, k_cache, v_cache, page_table, context_len, *, chunk_len=No
     P = page_table.shape[1]
     _need(page_table, "page_table", torch.int32, (B, P), dev)
     _need(context_len, "context_len", torch.int32, (B,), dev)
-    _opt(chunk_len, "chunk_len", torch.int32, (B,), dev)
-    _opt(parents, "parents", torch.int32, (B, T), dev)
-    _opt(lse, "lse", torch.float32, (B, T, Hq), dev)
+    if chunk_len is not None:
+        _need(chunk_len, "chunk_len", torch.int32, (B,), dev)
+    if parents is not None:
+        _need(parents, "parents", torch.int32, (B, T), dev)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, (B, T, Hq), dev)
     if workspace is None:
         workspace = make_attention_workspace(T, Hq, H, D, dev)
     elif not isinstance(workspace, torch.Tensor) or workspace.device != dev or not workspace.is_contiguous():
