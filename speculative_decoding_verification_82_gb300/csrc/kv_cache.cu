@@ -12,7 +12,7 @@
 // draft tree's few rows.  A row belongs to the smallest power of two of lanes that covers it with 16 (8 where
 // head_dim asks for it) elements each, 8 lanes for 128, so its maximum is a few shuffles and every lane moves
 // whole 16-byte vectors of codes; a thread has two rows in flight.  (One row and 8 elements a thread:
-// 46 us where this takes 36 on 16 x 2052 tokens of 8 heads of 128 read to bf16, 15.5 where this takes 14.2
+// 46 us where this takes 36 on 16 x 2052 tokens of 8 heads of 128 read to bf16, 15.5 where this takes 12.2
 // on 4 x 2048 f16 tokens written.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -42,15 +42,15 @@ struct KvRows {
   specv::FastDiv fd_2h;         // rows of one token (K heads, then V heads)
 };
 
-// 8 elements of a row as floats, and back.
+// 8 elements of a row (their words) as floats, and back.
 template <typename T>
 struct Vec8;
 template <>
 struct Vec8<float> {
   static constexpr int kBytes = 32;
-  __device__ static void load(const unsigned char* p, float (&f)[8]) {
-    const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  __device__ static void unpack(const uint32_t* w, float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
   }
   __device__ static void store(unsigned char* p, const float (&f)[8]) {
     reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
@@ -60,9 +60,7 @@ struct Vec8<float> {
 template <>
 struct Vec8<__nv_bfloat16> {
   static constexpr int kBytes = 16;
-  __device__ static void load(const unsigned char* p, float (&f)[8]) {
-    const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p));
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  __device__ static void unpack(const uint32_t* w, float (&f)[8]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       f[2 * i] = __uint_as_float(w[i] << 16);
@@ -82,9 +80,7 @@ struct Vec8<__nv_bfloat16> {
 template <>
 struct Vec8<__half> {
   static constexpr int kBytes = 16;
-  __device__ static void load(const unsigned char* p, float (&f)[8]) {
-    const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p));
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  __device__ static void unpack(const uint32_t* w, float (&f)[8]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
@@ -150,10 +146,10 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const KvRows P) {
   const unsigned lanes = 1u << P.lanes_log2;
   const int e0 = (int)(threadIdx.x & (lanes - 1)) * E;
   const bool in = e0 < P.D;
-  const unsigned char* src[kRowsPerThread];
-  size_t at[kRowsPerThread];  // the row's first element in the cache
-  int kv[kRowsPerThread];     // 0 K, 1 V, -1 nothing to write
-  float x[kRowsPerThread][E];
+  constexpr int W = E * S / 4;  // words of a lane's elements
+  size_t at[kRowsPerThread];    // the row in the cache
+  int kv[kRowsPerThread];       // 0 K, 1 V, -1 nothing to write
+  uint32_t raw[kRowsPerThread][W];
 #pragma unroll
   for (int u = 0; u < kRowsPerThread; ++u) {
     const unsigned row = row_of<E>(P, u);
@@ -165,26 +161,25 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const KvRows P) {
     if (slot < 0 || slot >= P.num_slots) continue;
     kv[u] = h >= P.H ? 1 : 0;
     h -= kv[u] ? P.H : 0;
-    src[u] = P.src[kv[u]] + (long long)n * P.stride[kv[u]] + ((size_t)h * P.D + e0) * S;
-    at[u] = ((size_t)slot * P.H + h) * P.D;
-    if (QUANT) {
+    const unsigned char* src = P.src[kv[u]] + (long long)n * P.stride[kv[u]] + ((size_t)h * P.D + e0) * S;
+    at[u] = (size_t)slot * P.H + h;
 #pragma unroll
-      for (int i = 0; i < E; i += 8) {
-        float(&y)[8] = reinterpret_cast<float(&)[8]>(x[u][i]);
-#pragma unroll
-        for (int z = 0; z < 8; ++z) y[z] = 0.f;
-        if (in) Vec8<T>::load(src[u] + i * S, y);
-      }
+    for (int i = 0; i < W; i += 4) {
+      const uint4 v = in ? __ldcs(reinterpret_cast<const uint4*>(src + i * 4)) : make_uint4(0, 0, 0, 0);
+      raw[u][i] = v.x, raw[u][i + 1] = v.y, raw[u][i + 2] = v.z, raw[u][i + 3] = v.w;
     }
   }
 #pragma unroll
   for (int u = 0; u < kRowsPerThread; ++u) {
     if (kv[u] < 0) continue;
     if constexpr (QUANT) {
+      float x[E];
+#pragma unroll
+      for (int i = 0; i < E; i += 8) Vec8<T>::unpack(raw[u] + i * S / 4, reinterpret_cast<float(&)[8]>(x[i]));
       float a = 0.f;
 #pragma unroll
       for (int i = 0; i < E; ++i) {
-        const float m = fabsf(x[u][i]);
+        const float m = fabsf(x[i]);
         a = fmaxf(a, m < INFINITY ? m : 0.f);
       }
       const unsigned group = (lanes == 32 ? 0xffffffffu : ((1u << lanes) - 1u)) << ((threadIdx.x & 31) & ~(lanes - 1));
@@ -197,24 +192,23 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const KvRows P) {
         float y[4];
 #pragma unroll
         for (int z = 0; z < 4; ++z) {
-          y[z] = x[u][4 * i + z] * inv;
+          y[z] = x[4 * i + z] * inv;
           y[z] = fabsf(y[z]) <= 448.f ? y[z] : NAN;  // infinities (finite elements are within 448)
         }
         c[i] = e4m3x2(y[0], y[1]) | (e4m3x2(y[2], y[3]) << 16);
       }
       if (in) {
-        unsigned char* dst = P.dst[kv[u]] + at[u] + e0;
+        unsigned char* dst = P.dst[kv[u]] + at[u] * P.D + e0;
         if constexpr (E == 16)
           *reinterpret_cast<uint4*>(dst) = make_uint4(c[0], c[1], c[2], c[3]);
         else
           *reinterpret_cast<uint2*>(dst) = make_uint2(c[0], c[1]);
       }
-      if (e0 == 0) P.scale_out[kv[u]][at[u] / P.D] = pow2f_int(e);
+      if (e0 == 0) P.scale_out[kv[u]][at[u]] = pow2f_int(e);
     } else if (in) {
-      const uint4* s = reinterpret_cast<const uint4*>(src[u]);
-      uint4* d = reinterpret_cast<uint4*>(P.dst[kv[u]] + (at[u] + e0) * S);
+      uint4* d = reinterpret_cast<uint4*>(P.dst[kv[u]] + (at[u] * P.D + e0) * S);
 #pragma unroll
-      for (int i = 0; i < E * S / 16; ++i) d[i] = __ldcs(s + i);
+      for (int i = 0; i < W / 4; ++i) d[i] = make_uint4(raw[u][4 * i], raw[u][4 * i + 1], raw[u][4 * i + 2], raw[u][4 * i + 3]);
     }
   }
   check_slots(P);
