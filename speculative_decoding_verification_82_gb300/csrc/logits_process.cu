@@ -13,7 +13,9 @@
 //   4. it goes over the listed tokens of every row, spread evenly over its threads, and applies their rules
 //      to the input's logits (a few hundred elements of a block's 65,536, most of them in the chunks of the
 //      frequent, small ids: handled where their vectors stream, they held up whole warps and blocks:
-//      134 -> 121 us on 16 61-node trees of 128,256 bf16 logits; four rows in flight and groups of 8: 107).
+//      134 -> 121 us on 16 61-node trees of 128,256 bf16 logits; several rows in flight and groups of 8: 107).
+// The rows are prefetched to L2 ahead of step 1 (107 -> 105) and stored without staying in L1 or long in L2 (80.1 -> 78.7
+// on 64 chains of 6 f32 rows).
 // Mask bits are read at any offset, so rows whose start is not 16-byte aligned (an odd vocabulary) take the
 // same steps, with partial vectors at their ends.  Each logit is read and written once: the kernel is bound by
 // HBM bandwidth.  In place (out == logits), a vector that no rule touches is neither read nor written.
@@ -35,7 +37,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxRows = SPEC_MAX_LOGITS_ROWS;
 constexpr int kMaxChunk = 4096;  // tokens per block
-constexpr int kRowsAtOnce = 4;   // rows whose vectors a thread has in flight together
 constexpr int kMaxGroup = 8;     // rows per block (16 and 61 rows: 115 and 121 us where 8 take 108)
 constexpr int kScan = 8;         // history tokens a thread has in flight
 constexpr uint32_t kPromptBit = 0x80000000u, kBiasBit = 0x40000000u, kCountMask = 0x3fffffffu;
@@ -94,9 +95,19 @@ __device__ __forceinline__ float apply_rules(float x, uint32_t entry, uint32_t p
   return x;
 }
 
-// ALIGNED: every row starts on a 16-byte boundary, in both buffers.
-template <typename T, bool ALIGNED>
-__global__ void __launch_bounds__(kThreads, sizeof(typename Fmt<T>::Raw) == 4 ? 4 : 6) logits_process_kernel(const LogitsParams P) {
+// Rows whose vectors a thread has in flight together, and blocks an SM: few rows and many blocks where mask words come
+// before the vectors, more rows otherwise.  (16 trees of 61 rows of 128,256 bf16: with masks 100.7 us as here, 105 with 4 rows
+// and 6 blocks; without 80.5, and 93 with 2 rows and 8 blocks.  64 chains of 6 f32 rows without masks: 70.7, 80 with 4 rows
+// and 4 blocks.)
+template <typename T, bool MASKED>
+constexpr int kRowsAtOnce = sizeof(typename Fmt<T>::Raw) == 4 ? (MASKED ? 4 : 8) : (MASKED ? 2 : 4);
+template <typename T, bool MASKED>
+constexpr int kBlocks = sizeof(typename Fmt<T>::Raw) == 4 ? (MASKED ? 4 : 3) : (MASKED ? 8 : 6);
+
+// ALIGNED: every row starts on a 16-byte boundary, in both buffers.  MASKED: there are masks.
+template <typename T, bool ALIGNED, bool MASKED>
+__global__ void __launch_bounds__(kThreads, (kBlocks<T, MASKED>)) logits_process_kernel(const LogitsParams P) {
+  constexpr int kRows = kRowsAtOnce<T, MASKED>;
   constexpr int VE = Fmt<T>::VE, S = 16 / VE;
   using Raw = typename Fmt<T>::Raw;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -114,6 +125,15 @@ __global__ void __launch_bounds__(kThreads, sizeof(typename Fmt<T>::Raw) == 4 ? 
   const int t0 = chunk * P.chunk;
   const int t_end = min(P.V, t0 + span);
   const int words = span / 32 + 2;
+
+  const int r0 = group * P.rows_per_block, r1 = min(P.R, r0 + P.rows_per_block);
+  const int stop = min(P.V, t0 + P.chunk);
+  const bool in_place = P.in == P.out;
+  if (!in_place) {  // the rows are on their way to L2 meanwhile (in place, only what a mask forbids is read)
+    const unsigned char* in = P.in + (((size_t)b * P.R + r0) * (size_t)P.V + t0) * S;
+    for (int r = r0; r < r1; ++r, in += (size_t)P.V * S)
+      for (int o = 128 * t; o < (stop - t0) * S; o += 128 * kThreads) asm volatile("prefetch.global.L2 [%0];" ::"l"(in + o));
+  }
 
   // -- 1. the request's lengths, penalties and tree
   for (int i = t; i < span; i += kThreads) table[i] = 0;
@@ -206,11 +226,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(typename Fmt<T>::Raw) == 4 ? 
   __syncthreads();
 
   // -- 3. the rows' vectors
-  const bool in_place = P.in == P.out;
   constexpr uint32_t kAll = (1u << VE) - 1u;
   constexpr int per = VE / 4;  // elements of a word
-  const int r0 = group * P.rows_per_block, r1 = min(P.R, r0 + P.rows_per_block);
-  const int stop = min(P.V, t0 + P.chunk);
   const uint32_t inf = (uint32_t)Fmt<T>::raw(-INFINITY);
 
   auto forbid = [&](uint4& x, uint32_t ban) {  // -inf where ban has a bit
@@ -229,47 +246,50 @@ __global__ void __launch_bounds__(kThreads, sizeof(typename Fmt<T>::Raw) == 4 ? 
   };
 
   if constexpr (ALIGNED) {
-    // kRowsAtOnce rows at a time: their vectors are in flight together
-    for (int ra = r0; ra < r1; ra += kRowsAtOnce) {
+    // kRows rows at a time: their vectors are in flight together
+    for (int ra = r0; ra < r1; ra += kRows) {
       const size_t row = ((size_t)b * P.R + ra) * (size_t)P.V;
       const unsigned char* in = P.in + row * S;
       unsigned char* out = P.out + row * S;
-      const uint32_t* mask = P.allowed && !plain ? P.allowed + ((size_t)b * P.R + ra) * (size_t)P.W : nullptr;
+      const uint32_t* mask = MASKED && !plain ? P.allowed + ((size_t)b * P.R + ra) * (size_t)P.W : nullptr;
       if (in_place && !mask) break;
       const size_t pitch = (size_t)P.V * S;
-      bool has[kRowsAtOnce];
+      bool has[kRows];
 #pragma unroll
-      for (int u = 0; u < kRowsAtOnce; ++u) has[u] = ra + u < r1;
+      for (int u = 0; u < kRows; ++u) has[u] = ra + u < r1;
       for (int tk = t0 + t * VE; tk < stop; tk += kThreads * VE) {
-        uint4 x[kRowsAtOnce];
-        uint32_t ban[kRowsAtOnce];
+        uint4 x[kRows];
+        uint32_t ban[kRows];
 #pragma unroll
-        for (int u = 0; u < kRowsAtOnce; ++u)
+        for (int u = 0; u < kRows; ++u)
           ban[u] = mask && has[u] ? ~__ldg(mask + (size_t)u * P.W + (tk >> 5)) >> (tk & 31) & kAll : 0u;
 #pragma unroll
-        for (int u = 0; u < kRowsAtOnce; ++u)
-          if (has[u] && (!in_place || ban[u])) x[u] = *reinterpret_cast<const uint4*>(in + u * pitch + (size_t)tk * S);
+        for (int u = 0; u < kRows; ++u)
+          if (has[u] && (!in_place || ban[u])) {
+            const uint4* at = reinterpret_cast<const uint4*>(in + u * pitch + (size_t)tk * S);
+            x[u] = MASKED && per == 2 ? __ldcs(at) : *at;
+          }
 #pragma unroll
-        for (int u = 0; u < kRowsAtOnce; ++u) {
+        for (int u = 0; u < kRows; ++u) {
           if (ban[u]) forbid(x[u], ban[u]);
-          if (has[u] && (!in_place || ban[u])) *reinterpret_cast<uint4*>(out + u * pitch + (size_t)tk * S) = x[u];
+          if (has[u] && (!in_place || ban[u])) __stcs(reinterpret_cast<uint4*>(out + u * pitch + (size_t)tk * S), x[u]);
         }
       }
     }
   } else {
     // likewise, a row's vectors starting `a` elements before it: this block's are those whose first token lies
     // in [t0, stop), in block 0 also the one that starts before the row
-    for (int ra = r0; ra < r1; ra += kRowsAtOnce) {
+    for (int ra = r0; ra < r1; ra += kRows) {
       const size_t row = ((size_t)b * P.R + ra) * (size_t)P.V;
-      const uint32_t* mask = P.allowed && !plain ? P.allowed + ((size_t)b * P.R + ra) * (size_t)P.W : nullptr;
+      const uint32_t* mask = MASKED && !plain ? P.allowed + ((size_t)b * P.R + ra) * (size_t)P.W : nullptr;
       if (in_place && !mask) break;
       const size_t pitch = (size_t)P.V * S;
       for (int v = t0 / VE + t; v <= (stop + VE - 1) / VE; v += kThreads) {
-        uint4 x[kRowsAtOnce];
-        uint32_t ban[kRowsAtOnce];
-        int tk[kRowsAtOnce];  // the vector's first token; P.V: not this block's
+        uint4 x[kRows];
+        uint32_t ban[kRows];
+        int tk[kRows];  // the vector's first token; P.V: not this block's
 #pragma unroll
-        for (int u = 0; u < kRowsAtOnce; ++u) {
+        for (int u = 0; u < kRows; ++u) {
           const unsigned char* in = P.in + row * S + u * pitch;
           tk[u] = v * VE - (int)(((uintptr_t)in & 15u) / S);
           ban[u] = 0;
@@ -286,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(typename Fmt<T>::Raw) == 4 ? 
             x[u] = *reinterpret_cast<const uint4*>(in + (size_t)tk[u] * S);
         }
 #pragma unroll
-        for (int u = 0; u < kRowsAtOnce; ++u) {
+        for (int u = 0; u < kRows; ++u) {
           if (tk[u] >= P.V || (in_place && !ban[u])) continue;
           const unsigned char* in = P.in + row * S + u * pitch + (long long)tk[u] * S;
           unsigned char* out = P.out + row * S + u * pitch + (long long)tk[u] * S;
@@ -329,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(typename Fmt<T>::Raw) == 4 ? 
     for (int m = up[r]; m > 0; m = up[par[m]]) c += ltok[m] == l;
     const uint32_t entry = table[l];
     if (!entry && !c) continue;  // drafted, but not on this row's path
-    if (P.allowed && !(__ldg(P.allowed + ((size_t)b * P.R + r) * (size_t)P.W + (tok >> 5)) >> (tok & 31) & 1u)) continue;
+    if (MASKED && !(__ldg(P.allowed + ((size_t)b * P.R + r) * (size_t)P.W + (tok >> 5)) >> (tok & 31) & 1u)) continue;
     const float f = Fmt<T>::get(*reinterpret_cast<const Raw*>(P.in + (row + tok) * S), 0);
     *reinterpret_cast<Raw*>(P.out + (row + tok) * S) = Fmt<T>::raw(apply_rules(f, entry, c, q, (entry & kBiasBit) ? bias_sum[l] : 0.f));
   }
@@ -349,10 +369,9 @@ int sm_count_cached() {
 template <typename T>
 spec_status_t launch(const LogitsParams& P, unsigned grid, size_t smem, cudaStream_t stream) {
   const bool aligned = (((uintptr_t)P.in | (uintptr_t)P.out | ((uintptr_t)P.V * (16 / Fmt<T>::VE))) & 15u) == 0;
-  if (aligned)
-    logits_process_kernel<T, true><<<grid, kThreads, smem, stream>>>(P);
-  else
-    logits_process_kernel<T, false><<<grid, kThreads, smem, stream>>>(P);
+  auto* k = aligned ? (P.allowed ? logits_process_kernel<T, true, true> : logits_process_kernel<T, true, false>)
+                    : (P.allowed ? logits_process_kernel<T, false, true> : logits_process_kernel<T, false, false>);
+  k<<<grid, kThreads, smem, stream>>>(P);
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
