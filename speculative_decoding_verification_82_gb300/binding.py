@@ -337,7 +337,7 @@ _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambd
 def _call(fn, device, *args) -> None:
     """fn(*args, the current stream of `device`) with `device` current, its status checked.  Tensors among
     the arguments become their addresses."""
-    args = [a.data_ptr() if type(a) is Tensor or isinstance(a, Tensor) else a for a in args]
+    args = [a.data_ptr() if isinstance(a, Tensor) else a for a in args]
     index = device.index
     if index == _current_device():
         status = fn(*args, _current_stream(index))
@@ -367,7 +367,7 @@ def spec_logits_process(logits, *, history=None, history_len=None, prompt_len=No
     if logits.dtype not in DTYPE_CODE or logits.dim() != 3:
         raise TypeError("logits must be a [B][R][V] float32/bfloat16/float16 tensor")
     B, R, V = logits.shape
-    _need(logits, "logits", None, (B, R, V), dev)
+    _need(logits, "logits", logits.dtype, (B, R, V), dev)
     i32, f32 = torch.int32, torch.float32
     Lmax = 0
     if history is not None:
