@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<T, MASKED>)) logits_process
   __shared__ uint16_t par[kMaxRows], ltok[kMaxRows], up[kMaxRows];
   __shared__ uint32_t bitmap[kMaxChunk / 32 + 3];
   __shared__ int listed;
-  const int span = P.chunk + VE;  // tokens with an entry: a chunk's last vector may reach past its end
+  const int span = P.chunk + VE;  // places for tokens with an entry: a misaligned row's last vector reaches past the chunk
   uint32_t* table = reinterpret_cast<uint32_t*>(smem);
   uint16_t* list = reinterpret_cast<uint16_t*>(table + span);  // tokens with an entry or drafted, in any order
   float* bias_sum = reinterpret_cast<float*>(list + span);      // only with biases (span is even)
@@ -123,11 +123,13 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<T, MASKED>)) logits_process
   const int b = (int)(blockIdx.x - cg * P.fd_b.d), t = threadIdx.x;
   const int chunk = (int)specv::fdiv(cg, P.fd_groups), group = (int)cg - chunk * P.groups;
   const int t0 = chunk * P.chunk;
-  const int t_end = min(P.V, t0 + span);
+  const int stop = min(P.V, t0 + P.chunk);
+  // A token has one block: in place, a second one would apply its rules to what the first has written.  Aligned rows'
+  // vectors end with the chunk; of misaligned rows' tokens, step 4 takes those in this block's vectors.
+  const int t_end = ALIGNED ? stop : min(P.V, t0 + span);
   const int words = span / 32 + 2;
 
   const int r0 = group * P.rows_per_block, r1 = min(P.R, r0 + P.rows_per_block);
-  const int stop = min(P.V, t0 + P.chunk);
   const bool in_place = P.in == P.out;
   if (!in_place) {  // the rows are on their way to L2 meanwhile (in place, only what a mask forbids is read)
     const unsigned char* in = P.in + (((size_t)b * P.R + r0) * (size_t)P.V + t0) * S;
