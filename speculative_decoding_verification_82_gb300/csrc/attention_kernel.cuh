@@ -617,8 +617,10 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
         }
         if (warp_live) {
           // Scores to log2 units (c > 0).  e4m3: positions 32 w on are in units of 2^k[w], their V rows in units of
-          // 2^v[w].
+          // 2^v[w].  The factor is kept above zero: hidden scores are -inf, and -inf times 0 would be a NaN.  (Scores
+          // are below 2^33 here: where the product is below 2^-126 they are nothing against 1 either way.)
           const float* sc = exps + (E4M3 ? (kv + i) % ES * 12 : 0);
+          auto factor = [&](int w) { return E4M3 ? fmaxf(cq * sc[w], 0x1p-126f) : P.c; };
           // Two passes over the scores, 32 at a time, the next ones on their way: the maximum, then the
           // weights, which take the place of scores already read.
           uint32_t x[2][16];
@@ -641,7 +643,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
               most = fmaxf(most, fmaxf(m0, m1));
             }
             if constexpr (E4M3)
-              top = fmaxf(top, fmaf(most, cq * sc[w], sc[4 + w]));
+              top = fmaxf(top, fmaf(most, factor(w), sc[4 + w]));
             else
               top = fmaxf(top, most * P.c);
           }
@@ -674,7 +676,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
           const float mm = m == -INFINITY ? 0.f : -m;
 #pragma unroll kSteps
           for (int w = 0; w < 4; ++w) {
-            const float c = E4M3 ? cq * sc[w] : P.c, up = E4M3 ? mm + sc[4 + w] : mm;
+            const float c = factor(w), up = E4M3 ? mm + sc[4 + w] : mm;
             const float2 c2 = make_float2(c, c), m2 = make_float2(up, up);
             float2 s0 = make_float2(0.f, 0.f), s1 = s0;
 #pragma unroll
