@@ -617,10 +617,11 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
         }
         if (warp_live) {
           // Scores to log2 units (c > 0).  e4m3: positions 32 w on are in units of 2^k[w], their V rows in units of
-          // 2^v[w].  The factor is kept above zero: hidden scores are -inf, and -inf times 0 would be a NaN.  (Scores
-          // are below 2^33 here: where the product is below 2^-126 they are nothing against 1 either way.)
+          // 2^v[w].  The factor is kept above zero and finite: hidden scores are -inf, and -inf times 0 would be a NaN, as
+          // would 0 times infinity.  (Scores are below 2^33 here, and above 2^-48 or 0: where the product is below
+          // 2^-126 they are nothing against 1 either way, where it overflows they are above 2^80 or 0.)
           const float* sc = exps + (E4M3 ? (kv + i) % ES * 12 : 0);
-          auto factor = [&](int w) { return E4M3 ? fmaxf(cq * sc[w], 0x1p-126f) : P.c; };
+          auto factor = [&](int w) { return E4M3 ? fminf(fmaxf(cq * sc[w], 0x1p-126f), 0x1.fffffep127f) : P.c; };
           // Two passes over the scores, 32 at a time, the next ones on their way: the maximum, then the
           // weights, which take the place of scores already read.
           uint32_t x[2][16];
