@@ -414,8 +414,10 @@ spec_status_t spec_kv_read(const void *k_cache, const void *v_cache, spec_dtype_
  * weights become f16, each row in units of the largest scale among its 32 positions (32 i ..
  * 32 i + 31).  A scale that is a power of two, as spec_kv_write's are, loses nothing down to 2^-15
  * of that largest; another one is rounded to f16's 11 bits, as is its product with a code.  V scales
- * should lie within 2^-60 .. 2^100, and a bf16 query row's elements below 2^-38 of its largest are
- * rounded to that step.
+ * should lie within 2^-60 .. 2^100 (smaller ones count as 2^-60), and those of one request within
+ * 2^80 of each other: beyond that the weights of positions with the small ones may be lost from
+ * the softmax's sum.  A bf16 query row's elements below 2^-38 of its largest are rounded to that
+ * step.
  *
  * q              token n = b T + t at q + n q_stride (elements; a 16-byte multiple, pointer
  *                16-byte aligned): num_heads rows of head_dim elements, bf16 or f16 (f32:
