@@ -18,7 +18,7 @@ SOURCES = ["spec_verify_api.cu", "spec_verify_f32.cu", "spec_verify_bf16.cu", "s
            "spec_verify_static.cu", "spec_walk.cu",
            "ngram_draft.cu", "kv_compact.cu", "kv_cache.cu", "logits_process.cu", "attention.cu",
            "attention_bf16.cu", "attention_f16.cu"]
-HEADERS = ["verify_kernel.cuh", "verify_common.cuh", "tree_walk.cuh", "attention_kernel.cuh", "fastdiv.h"]
+HEADERS = ["verify_kernel.cuh", "verify_common.cuh", "tree_walk.cuh", "attention_kernel.cuh", "fastdiv.h", "device_info.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2"]
 

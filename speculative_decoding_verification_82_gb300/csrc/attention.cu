@@ -10,6 +10,7 @@
 #include <atomic>
 
 #include "attention_kernel.cuh"
+#include "device_info.h"
 #include "spec_verify.h"
 
 namespace specv {
@@ -41,17 +42,6 @@ Layout layout(long long rows, int D) {
   L.rec = L.ml + parts * UR * 8;
   L.total = (L.rec + kMaxCtas * sizeof(Record) + 255) / 256 * 256;
   return L;
-}
-
-int sm_count_cached() {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return -1;
-  static std::atomic<int> cache[64];
-  if (dev < 64 && cache[dev].load() > 0) return cache[dev].load();
-  int n = 0;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return -1;
-  if (dev < 64) cache[dev].store(n);
-  return n;
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -141,7 +131,7 @@ extern "C" spec_status_t spec_attention(const void* q, spec_dtype_t dtype, long 
   if (q_stride < (long long)num_heads * head_dim || q_stride % 8 != 0) return SPEC_ERR_INVALID_ARG;
   if (!workspace || ((uintptr_t)workspace & 255u) || workspace_bytes < spec_attention_workspace_bytes(T, num_heads, num_kv_heads, head_dim))
     return SPEC_ERR_WORKSPACE;
-  const int sms = sm_count_cached();
+  const int sms = specv::sm_count();
   if (sms <= 0) return SPEC_ERR_CUDA;
   const int G = num_heads / num_kv_heads;
   const long long rows = (long long)T * G;

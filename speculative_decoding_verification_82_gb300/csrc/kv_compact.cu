@@ -28,6 +28,7 @@
 // every byte it reads or writes.  Each CTA at once lets the next such launch do the same.
 #include <stdint.h>
 
+#include "device_info.h"
 #include "spec_verify.h"
 
 namespace {
@@ -135,17 +136,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_compact_kernel(const 
   }
 }
 
-int sm_count_cached() {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return -1;
-  static int cache[64] = {0};
-  if (dev < 64 && cache[dev] > 0) return cache[dev];
-  int n = 0;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return -1;
-  if (dev < 64) cache[dev] = n;
-  return n;
-}
-
 }  // namespace
 
 extern "C" spec_status_t spec_kv_compact(void* const* caches, int num_caches, long long num_slots, int row_bytes,
@@ -162,7 +152,7 @@ extern "C" spec_status_t spec_kv_compact(void* const* caches, int num_caches, lo
     if (!caches[i] || ((uintptr_t)caches[i] & 15u)) return SPEC_ERR_INVALID_ARG;
     P.caches[i] = static_cast<unsigned char*>(caches[i]);
   }
-  const int sms = sm_count_cached();
+  const int sms = specv::sm_count();
   if (sms <= 0) return SPEC_ERR_CUDA;
   // caches per CTA: about kCtasPerSm CTAs per SM over the (request, cache group) grid
   const long long target = (long long)kCtasPerSm * sms;

@@ -29,6 +29,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include "device_info.h"
 #include "fastdiv.h"
 #include "spec_verify.h"
 
@@ -357,17 +358,6 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<T, MASKED>)) logits_process
   }
 }
 
-int sm_count_cached() {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return -1;
-  static int cache[64] = {0};
-  if (dev < 64 && cache[dev] > 0) return cache[dev];
-  int n = 0;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return -1;
-  if (dev < 64) cache[dev] = n;
-  return n;
-}
-
 template <typename T>
 spec_status_t launch(const LogitsParams& P, unsigned grid, size_t smem, cudaStream_t stream) {
   const bool aligned = (((uintptr_t)P.in | (uintptr_t)P.out | ((uintptr_t)P.V * (16 / Fmt<T>::VE))) & 15u) == 0;
@@ -399,7 +389,7 @@ extern "C" spec_status_t spec_logits_process(const void* logits, spec_dtype_t dt
   if (num_biases > 0 && (!bias_tokens || !bias_values)) return SPEC_ERR_INVALID_ARG;
   const int S = dtype == SPEC_DTYPE_F32 ? 4 : 2;
   if (((uintptr_t)logits % S) || ((uintptr_t)out % S)) return SPEC_ERR_INVALID_ARG;
-  const int sms = sm_count_cached();
+  const int sms = specv::sm_count();
   if (sms <= 0) return SPEC_ERR_CUDA;
   LogitsParams P = {};
   P.in = static_cast<const unsigned char*>(logits);

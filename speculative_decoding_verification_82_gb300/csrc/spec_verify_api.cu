@@ -10,6 +10,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "device_info.h"
 #include "spec_verify.h"
 #include "verify_kernel.cuh"
 
@@ -87,19 +88,6 @@ Layout layout(int B, int rows, const Chunking& ck) {
   off = align_up(off + b * r * (size_t)ck.nchunk_r * G * sizeof(specv::TagSum), 256);
   L.total = off;
   return L;
-}
-
-// Multiprocessors of the current device (cached per device); *device receives the device.
-int sm_count(int* device) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return -1;
-  *device = dev;
-  static int cache[64] = {0};
-  if (dev < 64 && cache[dev] > 0) return cache[dev];
-  int n = 0;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return -1;
-  if (dev < 64) cache[dev] = n;
-  return n;
 }
 
 bool aligned_to(const void* p, int a) { return ((uintptr_t)p % (uintptr_t)a) == 0; }
@@ -237,7 +225,7 @@ spec_status_t verify_chain_common(bool ngram, const void* target, const void* dr
   spec_status_t st = attach_workspace(P, ws, ws_bytes, B, rows, ck);
   if (st != SPEC_OK) return st;
   int device = -1;
-  const int sms = sm_count(&device);
+  const int sms = specv::sm_count(&device);
   if (sms <= 0) return SPEC_ERR_CUDA;
   P.total = (unsigned)((long long)B * rows * ck.nchunk);
   P.total_r = (unsigned)((long long)B * P.npos * ck.nchunk_r);
@@ -344,7 +332,7 @@ spec_status_t spec_verify_tree_greedy(const void* target_logits, spec_dtype_t dt
   spec_status_t st = attach_workspace(P, workspace, workspace_bytes, B, rows, ck);
   if (st != SPEC_OK) return st;
   int device = -1;
-  const int sms = sm_count(&device);
+  const int sms = specv::sm_count(&device);
   if (sms <= 0) return SPEC_ERR_CUDA;
   P.total = (unsigned)((long long)B * rows * P.nchunk);
   P.npos = 0;
