@@ -432,7 +432,7 @@ spec_status_t spec_kv_read(const void *k_cache, const void *v_cache, spec_dtype_
  *                otherwise SPEC_ERRF_BAD_LENGTH.
  * parents        [B][T] int32 or NULL, as for spec_verify_tree_greedy (checked over the request's
  *                chunk_len tokens): SPEC_ERRF_BAD_TREE.
- * scale          > 0 and finite.
+ * scale          > 0, and scale log2(e) finite.
  * out            [B][T][num_heads][head_dim] dtype, 16-byte aligned; overlaps no input.
  * lse            [B][T][num_heads] float or NULL: log sum_j exp(scale q . k_j).
  * err_flags      [B] int32 or NULL.  A request with a bad length or tree gets zeros (lse -inf).  A

@@ -110,7 +110,7 @@ extern "C" spec_status_t spec_attention(const void* q, spec_dtype_t dtype, long 
   if (cache_dtype != dtype && cache_dtype != SPEC_DTYPE_E4M3) return SPEC_ERR_INVALID_ARG;
   if (B < 0 || T < 0 || num_heads < 1 || num_kv_heads < 1 || num_heads % num_kv_heads != 0) return SPEC_ERR_INVALID_ARG;
   if (num_pages < 0 || page_size < 1 || pages_per_request < 0) return SPEC_ERR_INVALID_ARG;
-  if (!(scale > 0.f) || isinf(scale)) return SPEC_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || isinf(scale * specv::attn::kLog2e)) return SPEC_ERR_INVALID_ARG;  // (0 times infinity is a NaN)
   if (head_dim != 64 && head_dim != 128) return SPEC_ERR_UNSUPPORTED;
   if (page_size < 8 || (page_size & (page_size - 1)) != 0 || num_pages > INT_MAX) return SPEC_ERR_UNSUPPORTED;
   if (parents && T > SPEC_MAX_WALK_NODES) return SPEC_ERR_UNSUPPORTED;
