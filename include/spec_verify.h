@@ -370,8 +370,8 @@ spec_status_t spec_logits_process(const void *logits, spec_dtype_t dtype, int B,
  * k, v           token n = b T + t at k + n k_stride (elements): num_kv_heads rows of head_dim
  *                contiguous elements; strides >= num_kv_heads * head_dim, 16-byte multiples, and
  *                16-byte aligned pointers (slices of a fused projection, say).
- * slots          [B][T] int32: each token's slot; -1 for no token (nothing is written).  Distinct:
- *                which of two tokens with one slot ends up there is undefined, row by row.
+ * slots          [B][T] int32: each token's slot; -1 for no token (nothing is written).  Distinct: a
+ *                slot that two tokens share holds elements of either, and either's scale.
  * k_cache, v_cache  [num_slots][num_kv_heads][head_dim] cache_dtype (dtype, or SPEC_DTYPE_E4M3).
  * k_scale, v_scale  [num_slots][num_kv_heads] float, e4m3 only (else ignored).
  * err_flags      [B] int32 or NULL: SPEC_ERRF_BAD_SLOT when a slot is outside [-1, num_slots); that
@@ -387,10 +387,11 @@ spec_status_t spec_kv_write(const void *k, const void *v, spec_dtype_t dtype, lo
                             long long num_slots, int32_t *err_flags, spec_stream_t stream);
 
 /*
- * Reading cache rows back: the values code * s of an e4m3 cache rounded once to dtype, or the
- * bits of a cache of that dtype.  A token with slot -1, or a bad one (SPEC_ERRF_BAD_SLOT), reads
- * zeros.  k_out, v_out: [B][T][num_kv_heads][head_dim] dtype, 16-byte aligned.  Otherwise as
- * spec_kv_write; slots need not be distinct.
+ * Reading cache rows back: the values code * s of an e4m3 cache in 32 bits (exact where s is a
+ * power of two, as spec_kv_write's are) rounded to dtype, or the bits of a cache of that dtype.  A
+ * token with slot -1, or a bad one (SPEC_ERRF_BAD_SLOT), reads zeros.  k_out, v_out:
+ * [B][T][num_kv_heads][head_dim] dtype, 16-byte aligned.  Otherwise as spec_kv_write; slots need
+ * not be distinct.
  */
 spec_status_t spec_kv_read(const void *k_cache, const void *v_cache, spec_dtype_t cache_dtype,
                            const float *k_scale, const float *v_scale, long long num_slots, int B,
@@ -435,8 +436,9 @@ spec_status_t spec_kv_read(const void *k_cache, const void *v_cache, spec_dtype_
  * scale          > 0, and scale log2(e) finite.
  * out            [B][T][num_heads][head_dim] dtype, 16-byte aligned; overlaps no input.
  * lse            [B][T][num_heads] float or NULL: log sum_j exp(scale q . k_j).
- * err_flags      [B] int32 or NULL.  A request with a bad length or tree gets zeros (lse -inf).  A
- *                page outside [0, num_pages) sets SPEC_ERRF_BAD_SLOT; its rows are read as zeros.
+ * err_flags      [B] int32 or NULL.  A request with a bad length gets zeros in all T rows (lse -inf),
+ *                one with a bad tree in its chunk_len rows.  A page outside [0, num_pages) sets
+ *                SPEC_ERRF_BAD_SLOT; its rows are read as zeros.
  * Masked and unwritten places never matter: a NaN or infinity in the K or V row of a token makes
  * the outputs of the queries that attend to it non-finite, in some or all dimensions, and of no
  * other query.
