@@ -176,6 +176,9 @@ extern "C" spec_status_t spec_attention(const void* q, spec_dtype_t dtype, long 
   A.out = static_cast<unsigned char*>(out);
   A.lse = lse;
   A.err_flags = err_flags;
+  // Units of a request side by side where there are two or four.  (bf16 chunks of 8 heads a KV head over 8192 positions, one
+  // after the other / side by side: 2 units 170 / 172 us, 4 units 309 / 294, 16 units 301 / 313.  Three and five to eight
+  // would gain 3 to 4% as well: 243 / 233, 298 / 287.)
   int ctas = sms < kMaxCtas ? sms : kMaxCtas;
   A.lanes = (A.nqp == 2 || A.nqp == 4) && ctas >= A.nqp ? A.nqp : 1;
   ctas -= ctas % A.lanes;

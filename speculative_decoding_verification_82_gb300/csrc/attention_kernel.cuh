@@ -34,9 +34,10 @@
 // abort flag, every role leaves, copies and products in flight are waited for, and the requests get
 // SPEC_ERRF_TIMEOUT.
 //
-// Measured, 64 query heads over 8 KV heads of 128: 64 chains of 6 tokens over 4096 bf16 positions 146 us (5.6 TB/s of K and V:
-// bound by HBM), over 8192 e4m3 positions 227 us (3.7 TB/s: bound by the codes' way to f16 beside the softmax); 16 trees of 61
-// nodes over 8192 156 us (1.26 PFLOP/s) and 2 x 2048 f16 tokens after 2048 290 us (1.18): a tile's products take 1,024 cycles
+// Measured, 64 query heads over 8 KV heads of 128: 64 chains of 6 tokens over 4096 bf16 positions 149 us (5.5 TB/s of K and V:
+// bound by HBM), over 8192 e4m3 positions 230 us (3.7 TB/s: bound by the codes' way to f16 beside the softmax); 16 trees of 61
+// nodes over 8192 157 us (1.25 PFLOP/s) and 2 x 2048 f16 tokens after 2048 295 us (1.17), both with pauses between the calls; after
+// seconds of calls the power cap lowers the clock, and they take 174 and 301.  A tile's products take 1,024 cycles
 // alone and 1,200-1,270 here, where the scores' operands come out of shared memory at all the 128 bytes a clock it has, and
 // two streams do not quite cover a softmax of 1,215 cycles and the products it waits for.
 #pragma once
