@@ -32,7 +32,7 @@
 // up the products: 64 chains over 4096 positions: 164 -> 151 us).  Warp 10: query rows and tree parents.  Warps
 // 12-15 and 16-19 (e4m3): K and V codes to 16 bits.  Every wait is bounded: one that gives up sets the CTA's
 // abort flag, every role leaves, copies and products in flight are waited for, and the requests get
-// SPEC_ERRF_TIMEOUT.
+// SPEC_ERRF_TIMEOUT; the joining kernel repeats it, since CTAs that start later write their requests' flags over it.
 //
 // Measured, 64 query heads over 8 KV heads of 128: 64 chains of 6 tokens over 4096 bf16 positions 149 us (5.5 TB/s of K and V:
 // bound by HBM), over 8192 e4m3 positions 230 us (3.7 TB/s: bound by the codes' way to f16 beside the softmax); 16 trees of 61
@@ -58,9 +58,10 @@ constexpr int kMaxCtas = 160;    // at most this many CTAs (the workspace's part
 constexpr int kMaxTree = SPEC_MAX_WALK_NODES;
 constexpr float kLog2e = 1.4426950408889634f;
 
+constexpr int kGaveUp = 1 << 30;
 struct Record {  // an item whose tiles several CTAs share: it starts in the CTA that writes the record
   int b, qp, h;  // b < 0: none
-  int last;      // the last CTA with a part of it (every P.lanes-th from this one on)
+  int last;      // the last CTA with a part of it (every P.lanes-th from this one on); kGaveUp: a wait of this CTA ran out
 };
 
 struct Params {
@@ -426,7 +427,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
       if (lane >= o) incl += v;
     }
     if (lane == 31) scan[warp] = incl;
-    if (tid == 0) P.rec[blockIdx.x].b = -1;
+    if (tid == 0) P.rec[blockIdx.x].b = -1, P.rec[blockIdx.x].last = 0;
     __syncthreads();  // (and before the one thread that may write the record)
     long long before = 0, total = 0;
     for (int w = 0; w < C::kThreads / 32; ++w) {
@@ -1224,6 +1225,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, PAIR>::kThreads, 1) attention_ker
   }
   if (*abort && P.err_flags)
     for (int b = tid; b < P.B; b += C::kThreads) atomicOr(P.err_flags + b, SPEC_ERRF_TIMEOUT);
+  if (*abort && tid == 0) P.rec[blockIdx.x].last |= kGaveUp;
 }
 
 // Joins the parts of the items that several CTAs share.  Block (c, y): the item that starts in CTA c, 8 of its
@@ -1236,11 +1238,15 @@ __global__ void __launch_bounds__(256) attention_combine_kernel(const __grid_con
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x;
   const Record rec = P.rec[c];
-  if (rec.b < 0) return;
+  auto pass_on = [&] {
+    if (!(rec.last & kGaveUp) || blockIdx.y != 0 || !P.err_flags) return;
+    for (int b = threadIdx.x; b < P.B; b += 256) atomicOr(P.err_flags + b, SPEC_ERRF_TIMEOUT);
+  };
+  if (rec.b < 0) return pass_on();
   const int n = P.chunk_len ? __ldg(P.chunk_len + rec.b) : P.T;
   const int rows = min((long long)UR, (long long)n * P.G - (long long)rec.qp * UR);
   const int row = blockIdx.y * R + threadIdx.x % R, q4 = threadIdx.x / R;
-  if (row >= rows) return;
+  if (row >= rows) return pass_on();
   const float2* ml = P.part_ml + row;
   const float4* po = reinterpret_cast<const float4*>(P.part_o) + (size_t)q4 * UR + row;
   auto slot = [&](int x) { return (size_t)(2 * x + (x == c)); };
@@ -1254,7 +1260,8 @@ __global__ void __launch_bounds__(256) attention_combine_kernel(const __grid_con
   l = v0.y * w0 + v1.y * w1;
   if (v0.y != v0.y || v1.y != v1.y) l = NAN;
   float4 o = make_float4(fmaf(p1.x, w1, p0.x * w0), fmaf(p1.y, w1, p0.y * w0), fmaf(p1.z, w1, p0.z * w0), fmaf(p1.w, w1, p0.w * w0));
-  for (int x = second + P.lanes; x <= rec.last; x += P.lanes) {
+  const int last = rec.last & ~kGaveUp;
+  for (int x = second + P.lanes; x <= last; x += P.lanes) {
     const float2 v = ml[slot(x) * UR];
     const float4 p = po[slot(x) * (D / 4) * UR];
     const float N = fmaxf(M, v.x), a = factor(M, N), w = factor(v.x, N);
@@ -1270,6 +1277,7 @@ __global__ void __launch_bounds__(256) attention_combine_kernel(const __grid_con
   w2.y = Half<T>::pack(o.z * inv, o.w * inv);
   *reinterpret_cast<uint2*>(P.out + (orow * D + 4 * q4) * 2) = w2;
   if (q4 == 0 && P.lse) P.lse[orow] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
+  pass_on();
 }
 
 // Launches both kernels on `stream`.
