@@ -191,11 +191,13 @@ SPECV_HD void weight_series(V r, V rl, V& z, V& tail) {
 template <typename V>
 SPECV_HD void weight_power(V x, const WeightRow& R, V& at, V& z, V& tail) {
   V low = of<V>(0.f);
+  const V given = x;
   x = at_least(x, R.least);
   if (R.far) {  // x - M and its rounding error
     const V m = of<V>(R.top), d = sub(x, m), back = sub(d, x);
     low = sub(sub(x, sub(d, back)), add(m, back));
-    x = at_least(d, -R.reach);  // (`least` may be a long way off, next to a large M)
+    // (`least` may be a long way off, next to a large M, or be M itself, the lowest float: what it raised is lowered again)
+    x = at_least(add(d, sub(given, x)), -R.reach);
   }
   const V np = mul(x, of<V>(-R.hi));  // -x c, as far as it goes
   at = add(np, of<V>(R.grid));
