@@ -72,7 +72,7 @@ __device__ __forceinline__ float2 turned(long long p, float w, float f) {
   const uint32_t quarter = (uint32_t)((turn + (1ull << 61)) >> 62);
   const long long rest = (long long)(turn - ((uint64_t)quarter << 62));  // within 2^61 of zero
   float s, c;
-  sincospif((float)(int)(rest >> 32) * 0x1p-31f, &s, &c);
+  sincospif(__ll2float_rn(rest) * 0x1p-63f, &s, &c);  // (all of it: small angles keep their 24 bits)
   float cs = quarter & 1 ? -s : c, sn = quarter & 1 ? c : s;
   if (quarter & 2) cs = -cs, sn = -sn;
   if (w < 0.f) sn = -sn;
