@@ -227,6 +227,13 @@ struct Row {  // one CTA's slice of a row
       cluster_barrier();
   }
 
+  // A logit's bits, not as constant data: rows may be filtered in place.
+  __device__ __forceinline__ static uint32_t bits_at(const unsigned char* p) {
+    if constexpr (S == 4)
+      return __ldcg(reinterpret_cast<const unsigned int*>(p));
+    else
+      return __ldcg(reinterpret_cast<const unsigned short*>(p));
+  }
   // Vector v of the slice; places outside the row are -inf.
   __device__ __forceinline__ uint4 fetch(int v) const {
     const int i0 = first + v * E;
@@ -235,7 +242,7 @@ struct Row {  // one CTA's slice of a row
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const bool in = i0 + e >= 0 && i0 + e < P.V;
-      const uint32_t x = in ? Elem<T>::load_raw(reinterpret_cast<const char*>(base) + ((long long)v * E + e) * S) : Elem<T>::kNegInf;
+      const uint32_t x = in ? bits_at(base + ((long long)v * E + e) * S) : Elem<T>::kNegInf;
       if constexpr (S == 4)
         words[e] = x;
       else
