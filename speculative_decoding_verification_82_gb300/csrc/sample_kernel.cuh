@@ -63,7 +63,7 @@ constexpr int kMostTokens = 1000 * kThreads;  // a CTA: a thread's sums stay wit
 constexpr int kCap = 1024;         // tokens that the leader can sort
 constexpr int kRanked = 128;       // up to so many it sorts by counting
 constexpr int kSegs = kMaxCluster * kWarps;
-constexpr int kMsg = 10;
+constexpr int kMsg = 8;
 constexpr uint32_t kLowest = 0x00800000u;  // the ordered bits of the lowest finite float
 constexpr float kLowestFloat = -3.402823466e38f;
 static_assert(kBins == 8 * kThreads && kCap == 4 * kThreads && kBoundBins == 4 * kThreads && kSegs == 64, "a thread's share");
