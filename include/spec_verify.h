@@ -463,8 +463,8 @@ spec_status_t spec_kv_read(const void *k_cache, const void *v_cache, spec_dtype_
  *                the scaling's factor on cosines and sines (1 without), finite.
  * positions      [B][T] int32 >= 0, or NULL: then context_len [B] int32 >= 0 (not both), and with it
  *                parents [B][T] int32 or NULL, as for spec_verify_tree_greedy.
- * q_out          rows as q's, q_out_stride elements apart; may be q itself (with q's stride), otherwise must
- *                not overlap an input.  Strides are 16-byte multiples, pointers 16-byte aligned.
+ * q_out          rows as q's, q_out_stride elements apart; may be q itself (with q's stride, and where k and v lie
+ *                apart from it), otherwise must not overlap an input.  Strides are 16-byte multiples, pointers 16-byte aligned.
  * err_flags      [B] int32 or NULL: SPEC_ERRF_BAD_SLOT as spec_kv_write; SPEC_ERRF_BAD_LENGTH for a negative
  *                position or context length; SPEC_ERRF_BAD_TREE for a malformed parent, looked at up to the
  *                request's last token that has a slot.  A token with a bad slot, position or path to the root is

@@ -589,13 +589,22 @@ def rope_inv_freq(rotary_dim: int, base: float = 10000.0, *, scaling: str | None
     return f.to(device=device, dtype=torch.float32), mult
 
 
+def _rows_meet(n: int, a: int, sa: int, la: int, b: int, sb: int, lb: int, size: int) -> bool:
+    """Whether n rows of la elements from address a, sa elements apart, share a byte with n of lb from b, sb apart: exact for
+    equal strides (slices of one buffer), else whether the whole ranges meet."""
+    if n == 0 or b >= a + ((n - 1) * sa + la) * size or a >= b + ((n - 1) * sb + lb) * size:
+        return False
+    d = (b - a) % (sa * size)
+    return sa != sb or d < la * size or d + lb * size > sa * size
+
+
 def spec_rope_kv_write(k, v, k_cache, v_cache, slots, inv_freq, *, q=None, positions=None, context_len=None, parents=None,
                        interleaved=False, factor=1.0, k_scale=None, v_scale=None, out=None) -> dict:
     """Rotates q [B][T][Hq][D] (when given) and k [B][T][H][D] to their positions and writes k and v into the
     cache slots `slots` [B][T], as spec_kv_write.  inv_freq [R / 2] float32: the angles of the first R
     elements' pairs (see rope_inv_freq).  Positions: `positions` [B][T], or context_len [B] + the token's
     place in the chunk, or its depth in the tree `parents` [B][T].  The rotated q goes to out["q"], which
-    may be q itself.  See spec_verify.h."""
+    may be q itself if k and v lie apart from it.  See spec_verify.h."""
     lib = library()
     dev = _cuda(k, "k")
     dtype, shape = k.dtype, k.shape
@@ -641,13 +650,13 @@ def spec_rope_kv_write(k, v, k_cache, v_cache, slots, inv_freq, *, q=None, posit
             if not isinstance(qo, Tensor) or qo.dtype is not dtype or qo.shape != shape:
                 raise ValueError("out q must have q's shape and dtype")
             os_ = _token_stride(qo, "out q", B, T, Hq, D, dev)
-            a, c = qo.data_ptr(), q.data_ptr()
-            if a != c or os_ != qs:  # from the first byte to behind the last: a of the output, c of q, e of k, f of v
-                size, last, e, f = 4 if dtype is torch.float32 else 2, B * T - 1, k.data_ptr(), v.data_ptr()
-                b, row, kv = a + (last * os_ + Hq * D) * size, Hq * D, H * D
-                if (c < b and a < c + (last * qs + row) * size or e < b and a < e + (last * ks + kv) * size
-                        or f < b and a < f + (last * vs + kv) * size):
-                    raise ValueError("out q must be q itself or overlap no input")
+            # from the first byte to behind the last: a of the output, c of q, e of k, f of v
+            size, last, a, c, e, f = 4 if dtype is torch.float32 else 2, B * T - 1, qo.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr()
+            b, row, kv = a + (last * os_ + Hq * D) * size, Hq * D, H * D
+            if (c < b and a < c + (last * qs + row) * size and (a != c or os_ != qs) and _rows_meet(last + 1, a, os_, row, c, qs, row, size)
+                    or e < b and a < e + (last * ks + kv) * size and _rows_meet(last + 1, a, os_, row, e, ks, kv, size)
+                    or f < b and a < f + (last * vs + kv) * size and _rows_meet(last + 1, a, os_, row, f, vs, kv, size)):
+                raise ValueError("out q must be q itself, with k and v apart, or overlap no input")
     elif qo is not None:
         raise ValueError("out q needs q")
     ef = _out(out.get("err_flags"), "err_flags", torch.int32, (B,), dev)
