@@ -566,7 +566,9 @@ def rope_inv_freq(rotary_dim: int, base: float = 10000.0, *, scaling: str | None
     "linear" divides every angle by it (Chen et al., arXiv:2306.15595); "base" raises the base so that the
     slowest angle alone is divided by all of it; "parts" divides the angles that turn at most `slow` times in
     original_len positions, keeps those that turn `fast` times or more, ramps in between, and has the
-    factor 0.1 ln(factor) + 1 (Peng et al., arXiv:2309.00071)."""
+    factor 0.1 ln(factor) + 1 (Peng et al., arXiv:2309.00071).  It ramps over the turns, as that paper writes it; a
+    checkpoint served with a ramp over the pairs' numbers between two rounded bounds has other angles in between, and those are
+    to be passed to spec_rope_kv_write as they are."""
     if rotary_dim < 2 or rotary_dim % 2:
         raise ValueError("rotary_dim must be even and at least 2")
     if not (base > 0 and factor >= 1):
