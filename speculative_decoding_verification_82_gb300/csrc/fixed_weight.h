@@ -7,11 +7,12 @@
 // up once a row; the second is 1 + z + z^2/2 + z^3/6 + z^4/24, z = r ln 2, |z| < 0.011 (what is left out is below
 // 2^-39).  The product, two floats, is cut by rounded sums again: whole numbers of 2^-22 and what remains, whole numbers of
 // 2^-44; the sums' bit patterns, less the constants', are those numbers, and threads add them up in 32 bits.  Rows whose
-// maximum is too large for the constant's 128 are moved to a maximum of 0 first, the rounding errors kept.
+// maximum is too large for the constant's 128 are moved to a maximum of 0 first, the rounding errors kept.  -inf weighs
+// nothing, next to the lowest float as the maximum, too.
 //
 // A weight is off by 2^-37 of itself on average (root mean square), and never by more than 2^-33 of it and
-// 2^-44 (tests/test_fixed_weight.py).  Two elements at a time share most instructions, and a pass that sums weights
-// executes about 33 an element, reading and unpacking included (64-bit products and shifts of whole numbers instead: 89).
+// 2^-44 (tests/test_fixed_weight.py, tests/test_fixed_weight_lowest.py).  Two elements at a time share most instructions, and a pass that sums weights
+// executes about 30 an element, reading and unpacking included (64-bit products and shifts of whole numbers instead: 89).
 #pragma once
 
 #include <math.h>

@@ -62,10 +62,11 @@ spec_status_t run(const void* logits, spec_dtype_t dtype, int B, int R, int V, f
   // fill the SMs, one and a half or two and a half each, of slices above 16 KB; without top-k, which does little but read, also until
   // slices are 128 KB, as then what four CTAs an SM read again stays in L2 (80 MB of 129); and while there are fewer than six CTAs an
   // SM until they are 40,000 tokens where all are weighed (not where bf16 values are counted).
-  // us with 1 / 2 / 4 / 8 CTAs a row.  By top-k: 96 f32 rows of 128,256 filtered 35 / 29 / 25 / 35, 256 bf16 rows of 151,936
-  // 42 / 50 / 52 / 72, 384 f32 rows 84 / 102 / 101 / 119.  Drawn by top-p alone: 96 f32 rows 114 / 85 / 64 / 70, 384 251 / 222 / 197 /
-  // 222; 48 bf16 rows of 32,000 31 / 25 / 22 / 25, 192 41 / 35 / 46 / 65, 384 55 / 60 / 75 / 118.  768 bf16 rows of 128,256 filtered so
-  // 203 / 184 / 206 / 309; 256 drawn from without rules 83 / 79 / 68 / 73, filtered by top-p 68 / 66 / 78 / 118.  One f32 row by top-p, slices in shared memory or not, 22.7 / 27.2.
+  // us with 1 / 2 / 4 / 8 CTAs a row.  By top-k: 96 f32 rows of 128,256 filtered 36 / 31 / 25 / 37, 256 bf16 rows of 151,936
+  // 44 / 53 / 53 / 74, 384 f32 rows 84 / 101 / 101 / 122.  Drawn by top-p alone: 96 f32 rows 113 / 83 / 62 / 70, 384 244 / 221 / 198 /
+  // 225; 48 bf16 rows of 32,000 33 / 25 / 23 / 26, 192 41 / 35 / 46 / 65, 384 56 / 61 / 75 / 117.  768 bf16 rows of 128,256 filtered so
+  // 201 / 184 / 205 / 310; 256 drawn from without rules 80 / 74 / 65 / 71, filtered by top-p 72 / 68 / 79 / 118; 200 of 50,257 drawn from without
+  // rules 36 / 31 / 33 / 42.  One f32 row by top-p, slices in shared memory or not, 23.8 / 27.5.
   P.cl = 1;
   const bool in_smem = rows * kMaxCluster <= 2 * sms;
   const bool weighed = !top_k && !(out && dtype == SPEC_DTYPE_BF16);

@@ -29,9 +29,10 @@
 // Every CTA of a cluster takes the same path; the cluster barrier is the only wait.
 //
 // What bounds it (us; a copy of the rows at HBM's rate in brackets).  One row of 32,000 by top-k and top-p: latency of some ten
-// dependent steps, 10.4.  384 f32 rows of 128,256 filtered by top-k: 84 (59).  976 bf16 rows: filtered by top-p 234 (75): of a
+// dependent steps, 9.8.  384 f32 rows of 128,256 filtered by top-k: 82 (59): one wave of CTAs in step, in which nothing moves while
+// lists are gathered and sorted (drawn, without the writing, 49).  976 bf16 rows: filtered by top-p 232 (75): of a
 // row's 100 us or so the first reading takes a tenth, the counting two tenths, the leader's sums two, the writing three to four;
-// drawn without rules 226 (37, reading), weighing bound by instruction issue (about 33 a logit); drawn by top-p 382, the bins'
+// drawn without rules 213 (37, reading), weighing bound by instruction issue (about 30 a logit); drawn by top-p 374, the bins'
 // additions and the weighing in turn.
 #pragma once
 
